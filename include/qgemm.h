@@ -387,6 +387,152 @@ qg_status qgemm_score_config(qg_format f, int M, int N, int K, const qg_config* 
 qg_status qgemm_rank_configs(qg_format f, int M, int N, int K, qg_config* out, int max_out, double* est_us,
                              int* n_out);
 
+/* ------------------------------------------- around the quantised products -- */
+
+/* What a decoder layer has between its quantised products: the norm that
+ * makes a product's operand, the rotation and the cache of keys and values,
+ * and the attention that reads the cache.  The conventions above hold: device
+ * pointers, the caller's buffers and stream, host checks before any launch,
+ * no allocation, copy or synchronisation (each call can be captured).  Unlike
+ * qgemm_run's weights, everything is read after the wait on the preceding
+ * kernel of the stream.
+ * A row with a NaN or an infinity is quantised to scale NaN and codes 0 here
+ * (it reads back as NaN), NVFP4 excepted. */
+
+/* Norms before and after a block, with its gate, scales and residual:
+ *     b = P(x) * gate
+ *     h = residual_scale * residual + block_scale * b
+ *     y = N(h)
+ * P is post_norm and N pre_norm, each over the row's N elements:
+ *     QG_NORM_NONE   identity
+ *     QG_NORM_RMS    t / sqrt(mean(t^2) + eps) * (weight + weight_offset) + bias
+ *     QG_NORM_LAYER  the same of t - mean(t)
+ * All arithmetic is fp32; h is rounded once (to bf16), y once (to bf16, and
+ * from fp32 again to the operand's codes). */
+typedef enum { QG_NORM_NONE = 0, QG_NORM_RMS = 1, QG_NORM_LAYER = 2 } qg_norm_kind;
+
+#define QGEMM_NORM_MAX_WIDTH 32768
+
+typedef struct {
+  const void* residual;     /* bf16 [M, ldr]; NULL: 0                                */
+  const void* x;            /* bf16 [M, ldx], the block's output; NULL: 0            */
+  const void* gate;         /* bf16 [M, ldg], or one row [N] with ldg = 0; NULL: 1   */
+  const void* post_weight;  /* bf16 [N]; with post_norm, and only then               */
+  const void* post_bias;    /* bf16 [N] or NULL                                      */
+  const void* pre_weight;   /* bf16 [N]; with pre_norm, and only then                */
+  const void* pre_bias;     /* bf16 [N] or NULL                                      */
+  void* h;                  /* bf16 [M, ldh] out, NULL: not wanted; may be residual or
+                               x (same ld), in place                                 */
+  void* y;                  /* bf16 [M, ldy] out, NULL: not wanted                   */
+  int32_t ldr, ldx, ldg, ldh, ldy; /* elements, multiples of 8                       */
+  int32_t post_norm;        /* qg_norm_kind of P                                     */
+  int32_t pre_norm;         /* qg_norm_kind of N; QG_NORM_NONE: only h               */
+  float residual_scale, block_scale, eps, weight_offset;
+} qg_norm;
+
+/* `out` (NULL: not wanted) receives y as the activation operand of format f,
+ * as qgemm_quantize_act lays it out (rows M, K = N).  NVFP4 needs the amax of
+ * the whole tensor before any code, so it takes static_amax (device fp32
+ * scalar; without one QG_ERR_UNSUPPORTED).  N: a multiple of 8 (with `out`
+ * also of the format's K multiple), at most QGEMM_NORM_MAX_WIDTH. */
+qg_status qgemm_norm(const qg_norm* n, int M, int N, qg_format f, qg_operand* out, const float* static_amax,
+                     void* stream);
+
+/* A paged cache of keys and values, quantised per (token, head) row with the
+ * row formats: QG_FP8_DYNAMIC (e4m3, scale amax / 448) or QG_W8A8_INT8 (int8,
+ * scale amax / 127).  Place o of page g is slot g * page_size + o; its row of
+ * head h is row (g * kv_heads + h) * page_size + o of
+ *     k, v:             codes [pages, kv_heads, page_size, head_dim]
+ *     k_scale, v_scale: fp32  [pages, kv_heads, page_size]
+ * so that a page's rows of one head are contiguous.  head_dim 64 or 128,
+ * page_size a power of two from 16 to 1024 (QG_ERR_UNSUPPORTED otherwise, and
+ * for pages * kv_heads * page_size >= 2^31). */
+typedef struct {
+  qg_format format;
+  int32_t pages, page_size, kv_heads, head_dim;
+  void *k, *v;
+  float *k_scale, *v_scale;
+} qg_cache;
+
+/* Bytes of k (and of v), and of k_scale (and of v_scale). */
+qg_status qgemm_cache_bytes(qg_format f, int pages, int page_size, int kv_heads, int head_dim, size_t* code_bytes,
+                            size_t* scale_bytes);
+
+/* Writes `tokens` keys and values into their slots, and rotates queries and
+ * keys on the way.  Channel pair j < rope_dim / 2 of a head turns by
+ * positions[t] * frequency[j] radians (formed in 64 bits):
+ *     (a, b) -> magnitude * (a cos - b sin, b cos + a sin)
+ * with (a, b) = channels (j, j + rope_dim / 2), or (2j, 2j + 1) when
+ * interleaved; channels from rope_dim on, and values, stay.  Keys and values
+ * are quantised from fp32, queries rounded to bf16 once.
+ * A slot below 0 or past the cache is not written (a padded token); its query
+ * is still rotated.  The slots of a call must differ: a slot named twice ends
+ * up with one of the tokens' codes and, possibly, another's scale. */
+typedef struct {
+  const void *q, *k, *v;    /* bf16 [tokens, ld], head h at h * head_dim; q NULL: none */
+  void* q_out;              /* bf16 [tokens, ldqo]; may be q (same ld), in place     */
+  int32_t ldq, ldk, ldv, ldqo; /* elements, multiples of 8                           */
+  int32_t q_heads;          /* 0 without q                                           */
+  const int32_t* slots;     /* [tokens]                                              */
+  const int32_t* positions; /* [tokens], with rope_dim > 0                           */
+  const double* frequency;  /* [rope_dim / 2] radians per position                   */
+  int32_t rope_dim;         /* 0 (no rotation) .. head_dim, a multiple of 16         */
+  int32_t interleaved;
+  float magnitude;          /* factor on the rotated channels                        */
+} qg_cache_write;
+qg_status qgemm_cache_write(const qg_cache* c, const qg_cache_write* w, int tokens, void* stream);
+
+/* Reads slots back as bf16(code * scale) into k [tokens, ldk], v [tokens,
+ * ldv] (head h at h * head_dim).  Slots may repeat; one below 0 or past the
+ * cache gives a zero row. */
+qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, void* k, int ldk, void* v, int ldv,
+                           void* stream);
+
+#define QGEMM_ATTEND_MAX_Q 256
+
+/* Attention over the cache for the newest tokens of each sequence: single
+ * tokens, or trees of drafted tokens.
+ * Sequence b holds kv_len[b] positions, position p in place p % page_size of
+ * page page_table[b][p / page_size].  Its tokens q_offsets[b] ..
+ * q_offsets[b + 1] - 1 of q are its last positions, in order: drafted token i
+ * of n sits at position kv_len[b] - n + i (their keys and values have been
+ * written).  Every token sees all positions before the drafted ones, and the
+ * drafted tokens j whose bit is set in its row of tree_mask: bit j % 64 of
+ * word j / 64 of row q_offsets[b] + i (j from mask_words * 64 on: none).
+ * Without tree_mask token i sees drafted tokens j <= i.  For the set of
+ * positions a token sees, with key head h / (q_heads / kv_heads):
+ *     out = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+ * A token that sees nothing gets zeros and lse -inf.  Rows of out and lse that
+ * belong to no sequence are left as they were.  What a token does not see
+ * does not reach it, NaN rows included; a NaN row that it sees, key or value,
+ * makes its out and lse NaN.
+ * Device values are taken within bounds: offsets to [0, tokens], kv_len to
+ * [0, max_pages * page_size], pages to [0, pages); drafted tokens past max_q
+ * get no output.  batch <= 1024, max_q <= QGEMM_ATTEND_MAX_Q
+ * (QG_ERR_UNSUPPORTED).
+ * The queries are exact down to 2^-28 of their row's largest; weights are
+ * f16 relative to the largest |weight x value scale|, everything else fp32. */
+typedef struct {
+  const void* q;            /* bf16 [tokens, ldq], head h at h * head_dim            */
+  void* out;                /* bf16 [tokens, ldo]                                    */
+  float* lse;               /* fp32 [tokens, q_heads], NULL: not wanted              */
+  const int32_t* q_offsets; /* [batch + 1]                                           */
+  const int32_t* kv_len;    /* [batch]                                               */
+  const int32_t* page_table;/* [batch, max_pages]; entries past a sequence's last
+                               position are not read                                 */
+  const uint64_t* tree_mask;/* [tokens, mask_words]; NULL: causal                    */
+  int32_t mask_words;
+  int32_t ldq, ldo;         /* elements, multiples of 8                              */
+  int32_t q_heads;          /* a multiple of kv_heads                                */
+  int32_t batch, tokens, max_q, max_pages;
+  float scale;
+} qg_attend;
+
+/* Scratch bytes of qgemm_attend (needs no clearing; calls that may overlap on
+ * the GPU each need their own). */
+size_t qgemm_attend_workspace_size(const qg_cache* c, const qg_attend* a);
+qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------- table and tuning -- */
 
 /* Loads a per-shape table file written by qgemm_tune / qgemm_table_save.

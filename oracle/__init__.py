@@ -17,7 +17,8 @@ it uses fp32 exactly as the method's dynamic quantiser does):
 * the Split-K and Swap-AB rewrites of the same contraction ("Helion in the
   vLLM backend", second paragraph), which must leave the exact sums unchanged.
 
-Modules: ``formats`` (bit-level decode tables, nearest-even encoders, bf16
+Modules: ``layer`` (the operators between the products, imported by name),
+``formats`` (bit-level decode tables, nearest-even encoders, bf16
 rounding), ``quant`` (the four quantisers), ``gemm`` (the contraction and its
 epilogues).  Every function that has no independent pin says "parity
 unpinned" in its docstring; the pins live in ``tests/test_oracle_*.py``.

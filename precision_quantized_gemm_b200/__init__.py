@@ -9,12 +9,14 @@ first use; there is no fallback.
 The ctypes entry points carry the C names (``qgemm_run`` ...).  ``Operand``,
 ``quantize_act``, ``quantize_weight``, ``run`` and ``Linear`` are
 conveniences over them that allocate the caller-owned buffers with torch.
+``norm``, ``Cache``, ``Rope``, ``cache_write``, ``cache_read`` and ``attend``
+(layer.py) are the operators between a decoder layer's quantised products.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_double, c_int, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_size_t, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqgemm.so")
@@ -46,6 +48,8 @@ EXPORTS = [
     "qgemm_run_grouped", "qgemm_grouped_default_config", "qgemm_set_wait_limit", "qgemm_selftest_wait_expiry",
     "qgemm_set_tune_objective", "qgemm_grouped_act_bytes", "qgemm_quantize_act_grouped",
     "qgemm_quantize_weight_grouped", "qgemm_set_tma_store",
+    "qgemm_norm", "qgemm_cache_bytes", "qgemm_cache_write", "qgemm_cache_read", "qgemm_attend_workspace_size",
+    "qgemm_attend",
 ]
 
 
@@ -92,6 +96,38 @@ def skinny_config(tile_n=16, rows=32, stages=32) -> qg_config:
 class qg_operand(ctypes.Structure):
     _fields_ = [("q", c_void_p), ("scale", c_void_p), ("global_scale", c_void_p),
                 ("rows", c_int32), ("K", c_int32)]
+
+
+# norm kinds
+QG_NORM_NONE, QG_NORM_RMS, QG_NORM_LAYER = 0, 1, 2
+NORM_KINDS = {"none": QG_NORM_NONE, "rms": QG_NORM_RMS, "layer": QG_NORM_LAYER}
+QGEMM_ATTEND_MAX_Q = 256
+
+
+class qg_norm(ctypes.Structure):
+    _fields_ = ([(n, c_void_p) for n in ("residual", "x", "gate", "post_weight", "post_bias", "pre_weight", "pre_bias",
+                                         "h", "y")]
+                + [(n, c_int32) for n in ("ldr", "ldx", "ldg", "ldh", "ldy", "post_norm", "pre_norm")]
+                + [(n, c_float) for n in ("residual_scale", "block_scale", "eps", "weight_offset")])
+
+
+class qg_cache(ctypes.Structure):
+    _fields_ = ([("format", c_int)] + [(n, c_int32) for n in ("pages", "page_size", "kv_heads", "head_dim")]
+                + [(n, c_void_p) for n in ("k", "v", "k_scale", "v_scale")])
+
+
+class qg_cache_write(ctypes.Structure):
+    _fields_ = ([(n, c_void_p) for n in ("q", "k", "v", "q_out")]
+                + [(n, c_int32) for n in ("ldq", "ldk", "ldv", "ldqo", "q_heads")]
+                + [(n, c_void_p) for n in ("slots", "positions", "frequency")]
+                + [("rope_dim", c_int32), ("interleaved", c_int32), ("magnitude", c_float)])
+
+
+class qg_attend(ctypes.Structure):
+    _fields_ = ([(n, c_void_p) for n in ("q", "out", "lse", "q_offsets", "kv_len", "page_table", "tree_mask")]
+                + [(n, c_int32) for n in ("mask_words", "ldq", "ldo", "q_heads", "batch", "tokens", "max_q",
+                                          "max_pages")]
+                + [("scale", c_float)])
 
 
 class QGemmError(RuntimeError):
@@ -161,6 +197,13 @@ def lib() -> ctypes.CDLL:
             "qgemm_run_fused_act": (c_int, [c_int, c_void_p, c_int, POINTER(qg_operand), c_int, c_int, c_int,
                                             POINTER(qg_config), c_void_p, c_size_t, c_void_p, c_int, c_int,
                                             c_void_p, c_void_p]),
+            "qgemm_norm": (c_int, [POINTER(qg_norm), c_int, c_int, c_int, POINTER(qg_operand), c_void_p, c_void_p]),
+            "qgemm_cache_bytes": (c_int, [c_int, c_int, c_int, c_int, c_int, POINTER(c_size_t), POINTER(c_size_t)]),
+            "qgemm_cache_write": (c_int, [POINTER(qg_cache), POINTER(qg_cache_write), c_int, c_void_p]),
+            "qgemm_cache_read": (c_int, [POINTER(qg_cache), c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+                                         c_void_p]),
+            "qgemm_attend_workspace_size": (c_size_t, [POINTER(qg_cache), POINTER(qg_attend)]),
+            "qgemm_attend": (c_int, [POINTER(qg_cache), POINTER(qg_attend), c_void_p, c_size_t, c_void_p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -665,3 +708,7 @@ def _linear_capture(self, M: int, W: Operand | None = None, cfg: qg_config | Non
 
 
 Linear.capture = _linear_capture
+
+from .layer import (Cache, NormResult, Rope, attend, cache_read, cache_write, norm,  # noqa: E402
+                    qgemm_attend, qgemm_attend_workspace_size, qgemm_cache_bytes, qgemm_cache_read,
+                    qgemm_cache_write, qgemm_norm, rope_frequencies)

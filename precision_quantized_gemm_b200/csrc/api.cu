@@ -127,6 +127,32 @@ bool make_tmap_y(CUtensorMap* m, const void* Y, int N, int M, int ldy) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace qg {
+qg_status launch_state(LaunchState* out) {
+  DeviceInfo* d;
+  const qg_status s = device_info(&d);
+  if (s != QG_OK) return s;
+  *out = {d->sms > 0 ? d->sms : 148, d->err, g_pdl, g_wait_ns};
+  return QG_OK;
+}
+
+bool make_row_tmap(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || (row_bytes != 64 && row_bytes != 128)) return false;
+  cuuint64_t dims[2] = {row_bytes, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)row_bytes, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace qg
+
+namespace {
 // ---------------------------------------------------------------- checks --
 bool valid_format(int f) { return f >= QG_FP8_DYNAMIC && f <= QG_NVFP4; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -509,6 +535,10 @@ qg_status check_operand_impl(qg_format f, const qg_operand* o, int rows, int K) 
 }  // extern "C"
 
 namespace qg {
+qg_status check_operand_out(qg_format f, int rows, int K, const qg_operand* out) {
+  return check_quant_out(f, rows, K, out);
+}
+
 // Host-side argument checks of qgemm_run (no device work).
 qg_status check_run_args(qg_format f, const qg_operand* A, const qg_operand* W, int M, int N, int K,
                          const qg_config* cfg, void* workspace, size_t ws_bytes, void* Y, int ldy,

@@ -1,6 +1,7 @@
 // internal.h — declarations shared by the library's translation units.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -42,6 +43,78 @@ cudaError_t launch_quant_nvfp4(const void* X, int R, int K, int ldx, const float
                                void* q, void* sf, float* gscale, float* partial,
                                cudaStream_t st, bool pdl, const int* offsets = nullptr,
                                int experts = 0);
+
+// The launch state of the current device (api.cu): SM count, device error
+// word, programmatic dependent launch and the limit of in-kernel waits.
+struct LaunchState {
+  int sms;
+  unsigned int* err;
+  bool pdl;
+  unsigned long long wait_ns;
+};
+qg_status launch_state(LaunchState* out);
+// The operand of a rows x K activation has every buffer it needs (api.cu).
+qg_status check_operand_out(qg_format f, int rows, int K, const qg_operand* out);
+// A 2D byte tensor [rows, row_bytes], boxes of box_rows whole rows (64 or 128
+// bytes) with the swizzle of that width (api.cu).
+bool make_row_tmap(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+
+// Kernel parameters of the norm (norm.cu).
+struct NormParams {
+  const __nv_bfloat16 *residual, *x, *gate;
+  const uint4 *post_weight, *post_bias, *pre_weight, *pre_bias;
+  __nv_bfloat16 *h, *y;
+  uint8_t* q;                // operand codes, NULL: none
+  void* scale;
+  float* global_scale;       // NVFP4
+  const float* static_amax;  // NVFP4
+  int M, N, ldr, ldx, ldg, ldh, ldy, sf_cols;
+  int format, post_norm, pre_norm;
+  float residual_scale, block_scale, eps, weight_offset, inv_n;
+};
+cudaError_t launch_norm(const NormParams& p, cudaStream_t st, bool pdl);
+
+// Kernel parameters of the cache write and read (cache.cu).
+struct CacheWriteParams {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* q_out;
+  uint8_t *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  const int *slots, *positions;
+  const double* frequency;
+  int ldq, ldk, ldv, ldqo, q_heads, kv_heads, rope_dim, interleaved, page_shift, slots_total;
+  float magnitude;
+};
+cudaError_t launch_cache_write(const CacheWriteParams& p, int tokens, int head_dim, bool int8, cudaStream_t st,
+                               bool pdl);
+struct CacheReadParams {
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  __nv_bfloat16 *k, *v;
+  const int* slots;
+  int tokens, ldk, ldv, kv_heads, page_shift, slots_total;
+};
+cudaError_t launch_cache_read(const CacheReadParams& p, int head_dim, bool int8, cudaStream_t st, bool pdl);
+
+// Kernel parameters of the attention over the cache (attend.cu).
+struct AttendParams {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;                 // NULL: not wanted
+  const int *q_offsets, *kv_len, *table;
+  const unsigned long long* mask;  // NULL: causal
+  const float *k_scale, *v_scale;
+  float* partial;             // workspace
+  int ldq, ldo, ldp, mask_words, q_heads, kv_heads, group, batch, tokens, max_q;
+  int pages, page_shift, box_rows;
+  float scale_log2;           // softmax scale * log2(e)
+  unsigned int* err;
+  unsigned long long wait_ns;
+};
+constexpr int kAttendMaxBatch = 1024;
+size_t attend_workspace(int head_dim, int rows_max, int sms);
+cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+                          bool int8, int sms, cudaStream_t st, bool pdl);
 
 // GEMM launchers, one per format (each in its own translation unit).
 // Returns cudaErrorInvalidValue for a (swap, tile_n) pair not instantiated.

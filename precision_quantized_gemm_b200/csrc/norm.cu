@@ -1,0 +1,246 @@
+// norm.cu — the norms before and after a block, fused with the block's gate
+// and scales, the residual sum and the quantisation of the next product's
+// operand:
+//   b = P(x) * g                 P: none, or a norm with the post weight
+//   h = residual_scale * r + block_scale * b
+//   y = N(h)                     N: RMS or LayerNorm with the pre weight
+// h leaves as bf16, y as bf16 and / or as an operand of one of the four
+// formats.  Every sum, h and y are fp32: h and y are each rounded once, y
+// straight to the codes (no bf16 in between).
+//
+// Bound: HBM for many rows (each input read once, each output written once),
+// latency for few.  One CTA owns a row, which stays in registers (chunks of 8
+// elements per thread) between its up to five reductions.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "quant_math.cuh"
+#include "row_quant.cuh"
+
+namespace qg {
+namespace {
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum / unsigned maximum over the CTA, the same in every thread.  Each call
+// of a row takes its own 32 words of `red`, so one barrier is enough.
+__device__ __forceinline__ float cta_sum(float v, float* red) {
+  v = warp_sum(v);
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  if (l == 0) red[w] = v;
+  __syncthreads();
+  return warp_sum(l < (int)(blockDim.x >> 5) ? red[l] : 0.f);
+}
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  if (l == 0) red[w] = v;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, l < (int)(blockDim.x >> 5) ? red[l] : 0u);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint4 v;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+  return v;
+}
+
+// x <- norm(x) * (w + offset) + b over the row's `nch` chunks.
+template <int CH>
+__device__ __forceinline__ void norm_row(float (&x)[CH][8], int nch, float inv_n, bool layer, float eps,
+                                         const uint4* __restrict__ w, const uint4* __restrict__ b, float offset,
+                                         float* red) {
+  if (layer) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += x[i][j];
+    const float mean = cta_sum(s, red) * inv_n;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const bool in = threadIdx.x + i * blockDim.x < nch;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = in ? x[i][j] - mean : 0.f;
+    }
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q = fmaf(x[i][j], x[i][j], q);
+  const float r = rsqrtf(cta_sum(q, red + 32) * inv_n + eps);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    if (c < nch) {
+      float wv[8];
+      unpack8(__ldg(w + c), wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = x[i][j] * r * (wv[j] + offset);
+      if (b != nullptr) {
+        float bv[8];
+        unpack8(__ldg(b + c), bv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] += bv[j];
+      }
+    }
+  }
+}
+
+template <int CH>
+__global__ void __launch_bounds__(CH >= 8 ? 512 : 1024) norm_kernel(const NormParams p) {
+  __shared__ float red[160];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int m = blockIdx.x;
+  const int nch = p.N / 8;
+  const bool nvf4 = p.format == QG_NVFP4;
+  float g = 1.f;
+  if (nvf4) {
+    const float a = __ldg(p.static_amax);
+    g = a > 0.f ? __fdiv_rn(a, 2688.f) : 1.f;
+    if (m == 0 && threadIdx.x == 0) *p.global_scale = g;
+  }
+  if (m >= p.M) {  // the scale rows that pad the last 128-row atom
+    for (int c = threadIdx.x; c < p.sf_cols; c += blockDim.x)
+      static_cast<uint8_t*>(p.scale)[sf_offset(m, c, p.sf_cols)] = 0;
+    return;
+  }
+  const uint4* rr = p.residual ? reinterpret_cast<const uint4*>(p.residual + (size_t)m * p.ldr) : nullptr;
+  const uint4* xr = p.x ? reinterpret_cast<const uint4*>(p.x + (size_t)m * p.ldx) : nullptr;
+  const uint4* gr = p.gate ? reinterpret_cast<const uint4*>(p.gate + (size_t)m * p.ldg) : nullptr;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 rv[CH];
+  float v[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    rv[i] = rr && c < nch ? rr[c] : zero;
+    unpack8(xr && c < nch ? xr[c] : zero, v[i]);
+  }
+  if (p.post_norm)
+    norm_row<CH>(v, nch, p.inv_n, p.post_norm == QG_NORM_LAYER, p.eps, p.post_weight, p.post_bias, p.weight_offset,
+                 red);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    if (gr != nullptr && c < nch) {
+      float gv[8];
+      unpack8(gr[c], gv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= gv[j];
+    }
+    float r[8];
+    unpack8(rv[i], r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = fmaf(p.residual_scale, r[j], p.block_scale * v[i][j]);
+    if (p.h != nullptr && c < nch) reinterpret_cast<uint4*>(p.h + (size_t)m * p.ldh)[c] = pack8(v[i]);
+  }
+  if (!p.pre_norm) return;
+  norm_row<CH>(v, nch, p.inv_n, p.pre_norm == QG_NORM_LAYER, p.eps, p.pre_weight, p.pre_bias, p.weight_offset,
+               red + 64);
+  if (p.y != nullptr) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < nch) reinterpret_cast<uint4*>(p.y + (size_t)m * p.ldy)[c] = pack8(v[i]);
+    }
+  }
+  if (p.q == nullptr) return;
+  if (p.format == QG_FP8_DYNAMIC || p.format == QG_W8A8_INT8) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) a = max(a, absmax_bits8(v[i]));
+    a = cta_max(a, reinterpret_cast<uint32_t*>(red + 128));
+    const bool int8 = p.format == QG_W8A8_INT8;
+    const float s = int8 ? row_scale<true>(a) : row_scale<false>(a);
+    if (threadIdx.x == 0) static_cast<float*>(p.scale)[m] = s;
+    uint2* q = reinterpret_cast<uint2*>(p.q + (size_t)m * p.N);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < nch) q[c] = int8 ? row_codes<true>(v[i], s) : row_codes<false>(v[i], s);
+    }
+  } else if (p.format == QG_BLOCK_FP8) {
+    // a 128-element group is 16 chunks, held by 16 neighbouring threads
+    // (blockDim.x is a multiple of 32, N of 128)
+    uint2* q = reinterpret_cast<uint2*>(p.q + (size_t)m * p.N);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      uint32_t a = absmax_bits8(v[i]);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+      if (c < nch) {
+        const float s = row_scale<false>(a);
+        if ((c & 15) == 0) static_cast<float*>(p.scale)[(size_t)m * (p.N / 128) + c / 16] = s;
+        q[c] = row_codes<false>(v[i], s);
+      }
+    }
+  } else {
+    // NVFP4: a 16-element block is two neighbouring threads' chunks
+    uint32_t* q = reinterpret_cast<uint32_t*>(p.q + (size_t)m * (p.N / 2));
+    uint8_t* sf = static_cast<uint8_t*>(p.scale);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      const float own = absmax8(v[i]);
+      const float a = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, 1));
+      if (c < nch) {
+        const uint32_t code = cvt_e4m3x2(__fdiv_rn(__fdiv_rn(a, 6.f), g), 0.f) & 0xFF;
+        const float d = __fmul_rn(dec_e4m3(code), g);
+        uint32_t packed = 0;
+        if (d != 0.f) {
+          float t[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[j] = __fdiv_rn(v[i][j], d);
+          packed = cvt_e2m1x8(t);
+        }
+        q[c] = packed;
+        if ((c & 1) == 0) sf[sf_offset(m, c / 2, p.sf_cols)] = (uint8_t)code;
+      }
+    }
+    for (int c = p.N / 16 + threadIdx.x; c < p.sf_cols; c += blockDim.x) sf[sf_offset(m, c, p.sf_cols)] = 0;
+  }
+}
+
+template <int CH>
+cudaError_t launch_ch(const NormParams& p, int rows, int threads, cudaStream_t st, bool pdl) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, norm_kernel<CH>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormParams& p, cudaStream_t st, bool pdl) {
+  const int nch = p.N / 8;
+  // NVFP4 also writes the scale rows that pad the last 128-row atom
+  const int rows = p.q != nullptr && p.format == QG_NVFP4 ? (p.M + 127) / 128 * 128 : p.M;
+  auto threads = [&](int ch) { return ((nch + ch - 1) / ch + 31) / 32 * 32; };
+  if (threads(1) <= 1024 && p.M <= 2 * 148) return launch_ch<1>(p, rows, threads(1), st, pdl);
+  if (threads(2) <= 256) return launch_ch<2>(p, rows, threads(2), st, pdl);
+  if (threads(4) <= 1024) return launch_ch<4>(p, rows, threads(4), st, pdl);
+  return launch_ch<8>(p, rows, threads(8), st, pdl);
+}
+
+}  // namespace qg

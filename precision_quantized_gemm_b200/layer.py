@@ -1,0 +1,360 @@
+"""The operators between a decoder layer's quantised products: the norm that
+makes a product's operand, the rotary cache write, the cache read and the
+attention over the quantised cache.  Argument marshalling over the C ABI, as
+in the package's own module; the formulas stand in include/qgemm.h.
+
+    r = norm(residual, w, x, fmt=QG_FP8_DYNAMIC)          # r.h, r.operand
+    qkv = run(QG_FP8_DYNAMIC, r.operand, Wqkv).view(T, Hq + 2 * Hkv, D)
+    q, k, v = qkv.split([Hq, Hkv, Hkv], 1)
+    q = cache_write(cache, k, v, slots, q=q, rope=rope, positions=positions)
+    o = attend(cache, q, q_offsets, kv_len, page_table, tree_mask=mask)
+
+Shapes, types and strides are checked here (ValueError); sizes, alignment and
+options by the library (QGemmError).  ``stream``: the torch stream to launch
+on (default: the current stream of the tensors' device).  Buffers these
+functions allocate come from that stream's pool; tensors of other streams are
+the caller's to order, as with any torch operation.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from collections import namedtuple
+
+from . import (FORMATS, NORM_KINDS, QG_FP8_DYNAMIC, QG_NORM_NONE, QG_W8A8_INT8, QGEMM_ATTEND_MAX_Q, Operand, Workspace,
+               _torch, check, lib, qg_attend, qg_cache, qg_cache_write, qg_norm)
+
+__all__ = ["Cache", "NormResult", "Rope", "attend", "cache_read", "cache_write", "norm", "rope_frequencies"]
+
+NormResult = namedtuple("NormResult", "h y operand")
+
+
+# ------------------------------------------------------- C-named entry points --
+def qgemm_norm(n, M, N, fmt, out, static_amax_ptr, stream):
+    return lib().qgemm_norm(ctypes.byref(n), M, N, fmt, ctypes.byref(out) if out is not None else None,
+                            static_amax_ptr, stream)
+
+
+def qgemm_cache_bytes(fmt, pages, page_size, kv_heads, head_dim):
+    """(bytes of k or v, bytes of k_scale or v_scale) of a cache."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    check(lib().qgemm_cache_bytes(fmt, pages, page_size, kv_heads, head_dim, ctypes.byref(c), ctypes.byref(s)),
+          "qgemm_cache_bytes")
+    return c.value, s.value
+
+
+def qgemm_cache_write(cache, w, tokens, stream):
+    return lib().qgemm_cache_write(ctypes.byref(cache), ctypes.byref(w), tokens, stream)
+
+
+def qgemm_cache_read(cache, slots_ptr, tokens, k_ptr, ldk, v_ptr, ldv, stream):
+    return lib().qgemm_cache_read(ctypes.byref(cache), slots_ptr, tokens, k_ptr, ldk, v_ptr, ldv, stream)
+
+
+def qgemm_attend_workspace_size(cache, a):
+    return lib().qgemm_attend_workspace_size(ctypes.byref(cache), ctypes.byref(a))
+
+
+def qgemm_attend(cache, a, ws_ptr, ws_bytes, stream):
+    return lib().qgemm_attend(ctypes.byref(cache), ctypes.byref(a), ws_ptr, ws_bytes, stream)
+
+
+# ------------------------------------------------------------------- checking --
+class _On:
+    """Makes a tensor's device and the launch stream current, where they are not."""
+
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, device, stream):
+        self.dev, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self):
+        cuda = _torch().cuda
+        if self.dev.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        if self.stream is not None:
+            if self.stream.device != self.dev:
+                raise ValueError("the stream is not one of the tensors' device")
+            self.ctx = cuda.stream(self.stream)
+            self.ctx.__enter__()
+        elif self.dev.index != cuda.current_device():
+            self.ctx = cuda.device(self.dev)
+            self.ctx.__enter__()
+        return (self.stream or cuda.current_stream()).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _rows(name, t, rows, width, device):
+    """A bf16 matrix [rows, width] with contiguous rows; its row stride."""
+    if t.dtype != _torch().bfloat16 or t.shape != (rows, width) or t.device != device:
+        raise ValueError(f"{name}: bf16 [{rows}, {width}] on {device} wanted")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0) if rows > 1 else width
+
+
+def _heads(name, t, tokens, heads, dim, device):
+    """A bf16 tensor [tokens, heads, dim] whose heads lie side by side; its token stride."""
+    if t.dtype != _torch().bfloat16 or t.shape != (tokens, heads, dim) or t.device != device:
+        raise ValueError(f"{name}: bf16 [{tokens}, {heads}, {dim}] on {device} wanted")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
+        raise ValueError(f"{name}: a token's heads must lie side by side")
+    return st[0] if tokens > 1 else heads * dim
+
+
+def _ints(name, t, shape, device, dtype=None):
+    dtype = dtype or _torch().int32
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {device} wanted")
+    return t.data_ptr()
+
+
+def _vector(name, t, width, device):
+    if t is None:
+        return None
+    if t.dtype != _torch().bfloat16 or t.shape != (width,) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous bf16 [{width}] on {device} wanted")
+    return t.data_ptr()
+
+
+# ----------------------------------------------------------------------- norm --
+def norm(residual, weight, x=None, *, bias=None, kind="rms", post_weight=None, post_bias=None, gate=None,
+         block_scale=1.0, residual_scale=1.0, eps=1e-6, weight_offset=0.0, fmt=None, out=None, h=None, y=None,
+         static_amax=None, stream=None) -> NormResult:
+    """h = residual_scale * residual + block_scale * gate * P(x); y = norm(h).
+
+    ``residual`` (or None) and the block's output ``x`` (or None): bf16 [M, N].
+    ``kind``: "rms" or "layer", for the norm of h (``weight``, ``bias``; weight
+    None: only h) and for P (with ``post_weight``; else P is the identity).
+    ``gate``: bf16 [N] or [M, N].  ``fmt`` (a format): y becomes the operand
+    ``out`` (allocated if None) of the next ``run``; without it y is bf16.
+    ``h`` / ``y``: bf16 [M, N] buffers for them; h is also returned when x is
+    given or nothing else is asked for, and may be ``residual`` (in place).
+    NVFP4 needs ``static_amax``.  Returns NormResult(h, y, operand)."""
+    torch = _torch()
+    first = residual if residual is not None else x
+    if first is None or first.dim() != 2:
+        raise ValueError("residual or x: bf16 [M, N] wanted")
+    if kind not in ("rms", "layer"):
+        raise ValueError("kind is 'rms' or 'layer'")
+    M, N = first.shape
+    dev = first.device
+    if weight is None and (fmt is not None or out is not None or y is not None):
+        raise ValueError("y needs a weight")
+    if out is not None and fmt is None:
+        fmt = out.fmt
+    if out is not None and (out.fmt != fmt or out.is_weight):
+        raise ValueError("out is not an activation operand of this format")
+    code = NORM_KINDS[kind]
+    with _On(dev, stream) as st:
+        if h is None and (x is not None or weight is None):
+            h = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        if weight is not None and fmt is None and y is None:
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        if fmt is not None and out is None:
+            out = Operand(fmt, False, M, N, dev)
+        a = qg_norm()
+        for name, t, ld in (("residual", residual, "ldr"), ("x", x, "ldx"), ("h", h, "ldh"), ("y", y, "ldy")):
+            if t is not None:
+                setattr(a, ld, _rows(name, t, M, N, dev))
+                setattr(a, name, t.data_ptr())
+        if gate is not None:
+            if gate.dim() == 1:
+                a.gate = _vector("gate", gate, N, dev)
+            else:
+                a.ldg = _rows("gate", gate, M, N, dev)
+                a.gate = gate.data_ptr()
+        a.pre_weight, a.pre_bias = _vector("weight", weight, N, dev), _vector("bias", bias, N, dev)
+        a.post_weight, a.post_bias = _vector("post_weight", post_weight, N, dev), _vector("post_bias", post_bias, N, dev)
+        a.pre_norm = code if weight is not None else QG_NORM_NONE
+        a.post_norm = code if post_weight is not None else QG_NORM_NONE
+        a.residual_scale, a.block_scale, a.eps, a.weight_offset = residual_scale, block_scale, eps, weight_offset
+        amax = None
+        if static_amax is not None:
+            if static_amax.dtype != torch.float32 or static_amax.numel() != 1 or static_amax.device != dev:
+                raise ValueError(f"static_amax: one fp32 value on {dev} wanted")
+            amax = static_amax.data_ptr()
+        check(lib().qgemm_norm(a, M, N, fmt if fmt is not None else 0, out.c if out is not None else None, amax, st),
+              "qgemm_norm")
+    return NormResult(h, y, out)
+
+
+# ----------------------------------------------------------------------- rope --
+def rope_frequencies(dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original: int = 8192, low: float = 1.0, high: float = 4.0, fast: float = 32.0, slow: float = 1.0,
+                     device="cuda"):
+    """(frequency, magnitude) of a rotary embedding of ``dim`` channels:
+    frequency[j] = base^(-2j / dim) radians per position, float64 [dim / 2],
+    rescaled for contexts ``factor`` times the ``original`` one:
+      None      unscaled
+      "linear"  all frequencies / factor
+      "base"    base * factor^(dim / (dim - 2)): the slowest pair / factor, the fastest kept
+      "bands"   pairs that turn more than ``high`` times in the original context kept, fewer than ``low`` / factor,
+                a linear blend in the number of turns between
+      "ramp"    pairs that turn more than ``fast`` times kept, fewer than ``slow`` / factor, a linear blend in the
+                pair's index between; magnitude 0.1 ln(factor) + 1"""
+    torch = _torch()
+    if dim <= 0 or dim % 2 or factor < 1.0:
+        raise ValueError("dim: an even number; factor: at least 1")
+    j = torch.arange(dim // 2, dtype=torch.float64)
+    if scaling == "base":
+        base = base * factor ** (dim / (dim - 2)) if dim > 2 else base
+    f = float(base) ** (-2.0 * j / dim)
+    magnitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    elif scaling == "ramp":
+        def index(turns):  # the pair that turns so many times in the original context
+            return dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        first, last = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), dim // 2 - 1)
+        keep = 1 - ((j - first) / max(last - first, 1e-3)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+        magnitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling: None, 'linear', 'base', 'bands' or 'ramp'")
+    return f.to(device), magnitude
+
+
+class Rope:
+    """Rotary positions of a head's first ``2 * len(frequency)`` channels:
+    ``frequency`` float64 [R / 2] radians per position (rope_frequencies),
+    channel pairs (j, j + R / 2), or (2j, 2j + 1) when ``interleaved``."""
+
+    def __init__(self, frequency, interleaved: bool = False, magnitude: float = 1.0):
+        torch = _torch()
+        if frequency.dtype != torch.float64 or frequency.dim() != 1 or not frequency.is_contiguous():
+            raise ValueError("frequency: contiguous float64 [R / 2] wanted")
+        self.frequency, self.interleaved, self.magnitude = frequency, bool(interleaved), float(magnitude)
+        self.dim = 2 * frequency.numel()
+
+
+# ---------------------------------------------------------------------- cache --
+class Cache:
+    """A paged key / value cache quantised per (token, head): ``fmt``
+    QG_FP8_DYNAMIC (e4m3) or QG_W8A8_INT8.  Allocates zeroed buffers, or wraps
+    given ones: k, v uint8 [pages, kv_heads, page_size, head_dim], k_scale,
+    v_scale fp32 [pages, kv_heads, page_size].  Slot s is place s % page_size
+    of page s // page_size."""
+
+    def __init__(self, fmt: int, pages: int | None = None, page_size: int | None = None, kv_heads: int | None = None,
+                 head_dim: int | None = None, device="cuda", k=None, v=None, k_scale=None, v_scale=None):
+        torch = _torch()
+        if k is None:
+            if None in (pages, page_size, kv_heads, head_dim) or any(t is not None for t in (v, k_scale, v_scale)):
+                raise ValueError("pages, page_size, kv_heads and head_dim, or all four buffers, wanted")
+            qgemm_cache_bytes(fmt, pages, page_size, kv_heads, head_dim)
+            shape = (pages, kv_heads, page_size)
+            k, v = (torch.zeros(*shape, head_dim, dtype=torch.uint8, device=device) for _ in range(2))
+            k_scale, v_scale = (torch.zeros(*shape, dtype=torch.float32, device=device) for _ in range(2))
+        if k.dim() != 4:
+            raise ValueError("k: uint8 [pages, kv_heads, page_size, head_dim] wanted")
+        for name, t, shape, dtype in (("k", k, k.shape, torch.uint8), ("v", v, k.shape, torch.uint8),
+                                      ("k_scale", k_scale, k.shape[:3], torch.float32),
+                                      ("v_scale", v_scale, k.shape[:3], torch.float32)):
+            if t is None or t.dtype != dtype or t.shape != shape or t.device != k.device or not t.is_contiguous():
+                raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {k.device} wanted")
+        self.fmt = fmt
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        qgemm_cache_bytes(fmt, self.pages, self.page_size, self.kv_heads, self.head_dim)
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
+        self.c = qg_cache(fmt, self.pages, self.page_size, self.kv_heads, self.head_dim, k.data_ptr(), v.data_ptr(),
+                          k_scale.data_ptr(), v_scale.data_ptr())
+
+
+def cache_write(cache: Cache, k, v, slots, q=None, rope: Rope | None = None, positions=None, q_out=None, stream=None):
+    """Quantises keys and values (bf16 [T, kv_heads, head_dim], any token
+    stride) into the cache's ``slots`` (int32 [T]; below 0: a padded token,
+    not written; the others must differ), rotating keys by ``rope`` at
+    ``positions`` (int32 [T]).  ``q`` (bf16 [T, q_heads, head_dim]) is rotated
+    alongside into ``q_out`` (allocated if None, may be q), which is returned."""
+    torch = _torch()
+    if k.dim() != 3:
+        raise ValueError("k: bf16 [tokens, kv_heads, head_dim] wanted")
+    T, dev, D = k.shape[0], cache.device, cache.head_dim
+    with _On(dev, stream) as st:
+        a = qg_cache_write()
+        a.ldk, a.ldv = _heads("k", k, T, cache.kv_heads, D, dev), _heads("v", v, T, cache.kv_heads, D, dev)
+        a.k, a.v, a.slots = k.data_ptr(), v.data_ptr(), _ints("slots", slots, (T,), dev)
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError("q: bf16 [tokens, q_heads, head_dim] wanted")
+            a.q_heads = q.shape[1]
+            if q_out is None:
+                q_out = torch.empty(T, a.q_heads, D, dtype=torch.bfloat16, device=dev)
+            a.ldq, a.ldqo = _heads("q", q, T, a.q_heads, D, dev), _heads("q_out", q_out, T, a.q_heads, D, dev)
+            a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if rope is not None:
+            if positions is None or rope.frequency.device != dev:
+                raise ValueError(f"a rope needs positions, and its frequency on {dev}")
+            a.positions, a.frequency = _ints("positions", positions, (T,), dev), rope.frequency.data_ptr()
+            a.rope_dim, a.interleaved, a.magnitude = rope.dim, rope.interleaved, rope.magnitude
+        check(lib().qgemm_cache_write(cache.c, a, T, st), "qgemm_cache_write")
+    return q_out
+
+
+def cache_read(cache: Cache, slots, k=None, v=None, stream=None):
+    """Keys and values of ``slots`` (int32 [T]; below 0: a zero row) as bf16
+    [T, kv_heads, head_dim]; returns (k, v)."""
+    torch = _torch()
+    T, dev = slots.shape[0], cache.device
+    with _On(dev, stream) as st:
+        shape = (T, cache.kv_heads, cache.head_dim)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+        check(lib().qgemm_cache_read(cache.c, _ints("slots", slots, (T,), dev), T, k.data_ptr(),
+                                     _heads("k", k, *shape, dev), v.data_ptr(), _heads("v", v, *shape, dev), st),
+              "qgemm_cache_read")
+    return k, v
+
+
+# ------------------------------------------------------------------ attention --
+def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, scale: float | None = None,
+           max_q: int | None = None, out=None, lse=None, workspace: Workspace | None = None, stream=None):
+    """Attention of each sequence's newest tokens over the cache (qgemm_attend).
+
+    q: bf16 [T, q_heads, head_dim]; q_offsets int32 [B + 1]: sequence b's
+    tokens are rows q_offsets[b] .. q_offsets[b + 1]; kv_len int32 [B]: its
+    positions, those tokens' own (already written) included; page_table int32
+    [B, max_pages].  tree_mask int64 [T, words]: bit j of a token's words says
+    whether it sees its sequence's drafted token j (None: causal).  max_q: the
+    most tokens of one sequence (default: the most that T allows).  scale:
+    default head_dim ** -0.5.  lse: fp32 [T, q_heads] buffer for the log sums.
+    Returns out (bf16
+    [T, q_heads, head_dim]); rows that belong to no sequence are not written."""
+    torch = _torch()
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("q: bf16 [tokens, q_heads, head_dim], page_table: int32 [batch, max_pages] wanted")
+    T, Hq, D = q.shape
+    B, pages = page_table.shape
+    dev = cache.device
+    with _On(dev, stream) as st:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
+        a = qg_attend()
+        a.ldq, a.ldo = _heads("q", q, T, Hq, cache.head_dim, dev), _heads("out", out, T, Hq, D, dev)
+        a.q, a.out = q.data_ptr(), out.data_ptr()
+        a.q_offsets, a.kv_len = _ints("q_offsets", q_offsets, (B + 1,), dev), _ints("kv_len", kv_len, (B,), dev)
+        a.page_table = _ints("page_table", page_table, (B, pages), dev)
+        if lse is not None:
+            a.lse = _ints("lse", lse, (T, Hq), dev, torch.float32)
+        if tree_mask is not None:
+            if tree_mask.dim() != 2:
+                raise ValueError("tree_mask: int64 [tokens, words] wanted")
+            a.mask_words = tree_mask.shape[1]
+            a.tree_mask = _ints("tree_mask", tree_mask, (T, a.mask_words), dev, torch.int64)
+        a.q_heads, a.batch, a.tokens, a.max_pages = Hq, B, T, pages
+        a.max_q = min(T, QGEMM_ATTEND_MAX_Q) if max_q is None else max_q
+        a.scale = D ** -0.5 if scale is None else scale
+        workspace = workspace or Workspace(dev)
+        wsp, wsb = workspace.get(lib().qgemm_attend_workspace_size(cache.c, a))
+        check(lib().qgemm_attend(cache.c, a, wsp, wsb, st), "qgemm_attend")
+    return out
