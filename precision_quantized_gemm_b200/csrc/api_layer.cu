@@ -264,11 +264,14 @@ qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, s
   p.err = st.err;
   p.wait_ns = st.wait_ns;
   CUtensorMap tk, tv;
-  const uint64_t rows = (uint64_t)c->pages * c->kv_heads * c->page_size;
-  if (!qg::make_row_tmap(&tk, c->k, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;
-  if (!qg::make_row_tmap(&tv, c->v, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;
-  return qg::launch_attend(p, tk, tv, c->head_dim, c->format == QG_W8A8_INT8, st.sms, (cudaStream_t)stream, st.pdl) ==
-                 cudaSuccess
+  if (!qg::attend_tiles(a->max_q * group)) {
+    const uint64_t rows = (uint64_t)c->pages * c->kv_heads * c->page_size;
+    if (!qg::make_row_tmap(&tk, c->k, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;
+    if (!qg::make_row_tmap(&tv, c->v, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;
+  }
+  return qg::launch_attend(p, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), &tk, &tv,
+                           c->head_dim, c->format == QG_W8A8_INT8, st.sms, (cudaStream_t)stream,
+                           st.pdl) == cudaSuccess
              ? QG_OK
              : QG_ERR_CUDA;
 }

@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "attend_common.cuh"
+#include "attend_tile.cuh"
 #include "attr_cache.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -259,6 +260,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
       float top[2] = {m[0], m[1]};
       float2 sc[4][2];
+      uint32_t see[2] = {0, 0};  // bits of the block's positions from this lane's first on
+      if (tail) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) see[r] = (uint32_t)(seen_bits(p, x.tok0, tok[r], pos0, past, end) >> (2 * t));
+      }
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
         float2 ks;
@@ -269,11 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         for (int i = 0; i < 4; ++i) {
           const int e = i & 1, r = i >> 1;
           s[nt][i] = fmaf(s[nt][i] * row_scale[r], e ? ks.y : ks.x, sc[nt][e].x);
-          if (tail) {
-            const int pos = pos0 + nt * 8 + 2 * t + e;
-            const bool see = tok[r] >= 0 && pos < end && (pos < past || sees(p, x.tok0, tok[r], pos - past));
-            if (!see) s[nt][i] = kNegInf;
-          }
+          if (tail && !((see[r] >> (nt * 8 + e)) & 1)) s[nt][i] = kNegInf;
           top[r] = fmaxf(top[r], s[nt][i]);
         }
       }
@@ -533,6 +535,21 @@ cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& tk, const CUte
   return launch_pdl(fn, dim3(ctas), kWarps * 32, smem, args, st, pdl);
 }
 
+template <int D, bool INT8>
+cudaError_t launch_tile(const AttendParams& p, const uint8_t* k, const uint8_t* v, int ctas, cudaStream_t st,
+                        bool pdl) {
+  static GrowOnlyAttr opened;
+  const void* fn = (const void*)qg_attend_tile_kernel<D, INT8>;
+  constexpr int smem = TileSmem<D>::kTotal;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const int e = opened.ensure(
+      dev, smem, [&](int v) { return (int)cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v); });
+  if (e != 0) return (cudaError_t)e;
+  void* args[] = {(void*)&k, (void*)&v, (void*)&p};
+  return launch_pdl(fn, dim3(ctas), kTileThreads, smem, args, st, pdl);
+}
+
 template <int D>
 cudaError_t launch_merge(const AttendParams& p, int tile_rows, int unit, int ctas, cudaStream_t st, bool pdl) {
   void* args[] = {(void*)&p, (void*)&tile_rows, (void*)&unit};
@@ -541,21 +558,32 @@ cudaError_t launch_merge(const AttendParams& p, int tile_rows, int unit, int cta
 
 }  // namespace
 
+// More rows than one 16-row tile read the codes once per 16 rows in the rows
+// kernel; the tile kernel reads them once per 128.
+bool attend_tiles(int rows_max) { return rows_max > kRows; }
+
 size_t attend_workspace(int head_dim, int rows_max, int sms) {
-  (void)rows_max;
-  return (size_t)2 * sms * kRows * (head_dim + 2) * 4;
+  return (size_t)2 * sms * (attend_tiles(rows_max) ? kTileRows : kRows) * (head_dim + 2) * 4;
 }
 
-cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
-                          bool int8, int sms, cudaStream_t st, bool pdl) {
+cudaError_t launch_attend(const AttendParams& p, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
+                          const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl) {
+  const bool tiles = attend_tiles(p.max_q * p.group);
   cudaError_t e;
-  if (head_dim == 128)
-    e = int8 ? launch_rows<128, true>(p, tk, tv, sms, st, pdl) : launch_rows<128, false>(p, tk, tv, sms, st, pdl);
-  else
-    e = int8 ? launch_rows<64, true>(p, tk, tv, sms, st, pdl) : launch_rows<64, false>(p, tk, tv, sms, st, pdl);
+  if (tiles) {
+    if (head_dim == 128)
+      e = int8 ? launch_tile<128, true>(p, k, v, sms, st, pdl) : launch_tile<128, false>(p, k, v, sms, st, pdl);
+    else
+      e = int8 ? launch_tile<64, true>(p, k, v, sms, st, pdl) : launch_tile<64, false>(p, k, v, sms, st, pdl);
+  } else if (head_dim == 128) {
+    e = int8 ? launch_rows<128, true>(p, *tk, *tv, sms, st, pdl) : launch_rows<128, false>(p, *tk, *tv, sms, st, pdl);
+  } else {
+    e = int8 ? launch_rows<64, true>(p, *tk, *tv, sms, st, pdl) : launch_rows<64, false>(p, *tk, *tv, sms, st, pdl);
+  }
   if (e != cudaSuccess) return e;
-  return head_dim == 128 ? launch_merge<128>(p, kRows, kUnit, sms, st, pdl)
-                         : launch_merge<64>(p, kRows, kUnit, sms, st, pdl);
+  const int rows = tiles ? kTileRows : kRows, unit = tiles ? kTilePos : kUnit;
+  return head_dim == 128 ? launch_merge<128>(p, rows, unit, sms, st, pdl)
+                         : launch_merge<64>(p, rows, unit, sms, st, pdl);
 }
 
 }  // namespace qg

@@ -169,11 +169,31 @@ __device__ __forceinline__ Piece find_piece(const AttendParams& p, const long lo
   return x;
 }
 
-// Whether query token i of a sequence sees its drafted token j.
-__device__ __forceinline__ bool sees(const AttendParams& p, int tok0, int i, int j) {
-  if (p.mask == nullptr) return j <= i;
-  if (j >= p.mask_words * 64) return false;
-  return (__ldg(p.mask + (size_t)(tok0 + i) * p.mask_words + (j >> 6)) >> (j & 63)) & 1;
+// Which of the 64 positions from `pos0` on token i of a sequence sees, as bits:
+// the positions before the drafted ones, and the drafted tokens of its mask
+// row, up to `end`.  (i < 0: a row past the last, nothing.)
+__device__ __forceinline__ unsigned long long seen_bits(const AttendParams& p, int tok0, int i, int pos0, int past,
+                                                        int end) {
+  const int count = end - pos0, before = past - pos0;  // positions in range; those before the drafted ones
+  if (i < 0 || count <= 0) return 0ull;
+  const unsigned long long all = count >= 64 ? ~0ull : (1ull << count) - 1;
+  if (before >= 64) return all;
+  unsigned long long drafted;  // bit e: drafted token e - before (a negative one is not cached)
+  if (p.mask == nullptr) {
+    const int n = i + 1 + before;  // drafted tokens up to i
+    drafted = n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+  } else {
+    const unsigned long long* row = p.mask + (size_t)(tok0 + i) * p.mask_words;
+    if (before >= 0) {
+      drafted = __ldg(row) << before;
+    } else {
+      const int word = -before >> 6, shift = -before & 63;
+      drafted = word < p.mask_words ? __ldg(row + word) >> shift : 0ull;
+      if (shift && word + 1 < p.mask_words) drafted |= __ldg(row + word + 1) << (64 - shift);
+    }
+  }
+  const unsigned long long prefix = before > 0 ? (1ull << before) - 1 : 0ull;
+  return all & (prefix | drafted);
 }
 
 // Scale's log2 and reciprocal with the bounds of the header comment.
