@@ -50,8 +50,12 @@ qg_status check_attend(const qg_cache* c, const qg_attend* a) {
   if (a->tree_mask && (!aligned(a->tree_mask, 8) || a->mask_words <= 0)) return QG_ERR_INVALID_ARG;
   if (!(a->scale > -3.0e38f && a->scale < 3.0e38f)) return QG_ERR_INVALID_ARG;
   if (a->batch > qg::kAttendMaxBatch || a->max_q > QGEMM_ATTEND_MAX_Q) return QG_ERR_UNSUPPORTED;
-  // positions of a sequence are 32-bit
-  if (((long long)a->max_pages << shift_of(c->page_size)) > 0x7fffff00LL) return QG_ERR_UNSUPPORTED;
+  // positions of a sequence and units of work (at least 64 positions of 16
+  // rows of one key head) are 32-bit
+  const double positions = (double)a->max_pages * c->page_size;
+  const double tiles = (double)a->max_q * (a->q_heads / c->kv_heads) / 16 + 1;
+  if (positions > 0x7fffff00 || (positions / 64 + 1) * tiles * c->kv_heads * a->batch > 0x7fffff00)
+    return QG_ERR_UNSUPPORTED;
   return QG_OK;
 }
 

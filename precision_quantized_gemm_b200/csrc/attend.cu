@@ -87,8 +87,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   constexpr int KS = D / 16;   // MMA steps over the head's channels
   constexpr int NT = D / 8;    // 8-channel output tiles
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long pre[kAttendMaxBatch + 1];
-  __shared__ long long warp_tot[kWarps];
+  __shared__ Sched sched;
   __shared__ __align__(8) uint64_t bars[kWarps * kStages];
   __shared__ float2 vsc[kWarps][kBlock];       // (log2 vs, 1 / vs) of the block in hand
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
@@ -107,15 +106,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   fence_barrier_init();
   griddep_launch_dependents();
   griddep_wait();
-  scan_units(p, kRows, kUnit, pre, warp_tot);
-  const Share share = my_share(p, pre, gridDim.x, blockIdx.x);
+  const Share share = plan_units(p, kRows, kUnit, sched);
+  if (blockIdx.x >= share.ctas || share.total == 0) return;
+  const int share_begin = share.begin(blockIdx.x), share_end = share.begin(blockIdx.x + 1);
   uint32_t phase = 0;  // bit i: parity of the ring stage's next wait
   bool ok = true, drained = false;
 
-  for (long long u = share.begin; u < share.end;) {
-    const Piece x = find_piece(p, pre, kRows, kUnit, u, share.end);
-    const int begin = x.unit0 * kUnit, end = min(x.unit1 * kUnit, x.len);
-    const int past = x.len - x.n;               // position of drafted token 0
+#pragma unroll 1
+  for (int u = share_begin; u < share_end;) {
+    const Piece x = find_piece(p, sched, kRows, u, share_end);
+    const int tok0 = sched.tok0[x.seq], len = sched.len[x.seq];
+    const int rows = min(sched.n[x.seq], p.max_q) * p.group;
+    const int begin = x.unit0 * kUnit, end = min(x.unit1 * kUnit, len);
+    const int past = len - sched.n[x.seq];      // position of drafted token 0
     const int nblk = begin < end ? (end - begin + kBlock - 1) / kBlock : 0;
     const int* table = p.table + (size_t)x.seq * p.ldp;
 
@@ -157,11 +160,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     fence_proxy_async_smem();
     __syncwarp();
     int ahead = warp;
-    if (ok) {
-      for (int i = 0; i < kStages; ++i, ahead += kWarps)
-        if (ahead < nblk) issue(ahead, page_of(ahead));
-    }
     int next_page = page_of(ahead);
+    if (ok) {
+#pragma unroll 1
+      for (int i = 0; i < kStages; ++i) {
+        if (ahead < nblk) issue(ahead, next_page);
+        ahead += kWarps;
+        next_page = page_of(ahead);
+      }
+    }
 
     // queries of rows g and g + 8, f16, channels in the order of the key reads
     uint32_t qa[KS][4];
@@ -170,10 +177,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = x.row0 + g + 8 * i;
-      const bool live = row < x.rows;
+      const bool live = row < rows;
       tok[i] = live ? row / p.group : -1;
       const __nv_bfloat16* src =
-          p.q + (size_t)(x.tok0 + (live ? tok[i] : 0)) * p.ldq + (x.head * p.group + (live ? row % p.group : 0)) * D;
+          p.q + (size_t)(tok0 + (live ? tok[i] : 0)) * p.ldq + (x.head * p.group + (live ? row % p.group : 0)) * D;
       float amax = 0.f;
       uint4 raw[D / 32];  // 8 channels each
 #pragma unroll
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       uint32_t see[2] = {0, 0};  // bits of the block's positions from this lane's first on
       if (tail) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) see[r] = (uint32_t)(seen_bits(p, x.tok0, tok[r], pos0, past, end) >> (2 * t));
+        for (int r = 0; r < 2; ++r) see[r] = (uint32_t)(seen_bits(p, tok0, tok[r], end - pos0, past - pos0) >> (2 * t));
       }
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       __syncthreads();
     }
     const bool whole = x.unit0 == 0 && x.unit1 == x.units;
-    const int slot = 2 * blockIdx.x + (u == share.begin ? 0 : 1);
+    const int slot = 2 * blockIdx.x + (u == share_begin ? 0 : 1);
     float* part = p.partial + (size_t)slot * kRows * (D + 2);
     constexpr int TPR = kWarps * 32 / kRows;  // threads per row
     constexpr int CPT = D / TPR;              // channels per thread
@@ -422,8 +429,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     if (whole) {
       const int r = x.row0 + row;
-      if (r < x.rows) {
-        const size_t tk = x.tok0 + r / p.group;
+      if (r < rows) {
+        const size_t tk = tok0 + r / p.group;
         const int h = x.head * p.group + r % p.group;
         // a row that saw nothing: zeros, and a log-sum of -inf
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -451,58 +458,74 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 }
 
 // Merge of the items that span CTAs: CTA c takes the item that starts inside
-// share c and goes on past it (at most one), 16 rows per blockIdx.y.
+// share c and goes on past it (at most one), kMergeRows rows per blockIdx.y.
+// A warp takes one row of every fourth part, D / 32 channels a lane; the four
+// warps of a row meet in shared memory.
+constexpr int kMergeRows = 2;
 template <int D>
-__global__ void __launch_bounds__(256) qg_attend_merge_kernel(const AttendParams p, int tile_rows, int unit) {
-  __shared__ long long pre[kAttendMaxBatch + 1];
-  __shared__ long long warp_tot[8];
+__global__ void __launch_bounds__(kMergeRows * 128) qg_attend_merge_kernel(const AttendParams p, int tile_rows,
+                                                                           int unit) {
+  constexpr int CPL = D / 32;
+  __shared__ Sched sched;
+  __shared__ float acc_s[kMergeRows][4][D], sum_s[kMergeRows][4];
   griddep_launch_dependents();
   griddep_wait();
-  scan_units(p, tile_rows, unit, pre, warp_tot);
-  const Share s = my_share(p, pre, gridDim.x, blockIdx.x);
-  if (s.begin >= s.end || s.end >= s.total) return;
-  const Piece x = find_piece(p, pre, tile_rows, unit, s.end - 1, s.total);
-  const long long first = s.end - 1 - x.unit0;           // the item's first unit
-  if (first < s.begin || x.unit0 + 1 >= x.units) return;  // another CTA's, or done
-  const int last = share_of(s.total, s.ctas, first + x.units - 1);
-  constexpr int TPR = 16, CPT = D / TPR;
-  const int row = blockIdx.y * 16 + threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * CPT;
-  const int r = x.row0 + row;
-  if (r >= x.rows) return;
-  auto part_of = [&](int c) {
-    const int slot = 2 * c + (share_begin(s.total, s.ctas, c) < first ? 1 : 0);
-    return p.partial + (size_t)slot * tile_rows * (D + 2);
-  };
-  float top = kNegInf;
-  for (int c = blockIdx.x; c <= last; ++c) top = fmaxf(top, part_of(c)[tile_rows * D + row]);
-  float acc[CPT], sum = 0.f;
+  const Share s = plan_units(p, tile_rows, unit, sched);
+  if (blockIdx.x + 1 >= s.ctas) return;  // nothing goes on past the last share
+  const int begin = s.begin(blockIdx.x), end = s.begin(blockIdx.x + 1);
+  const Piece x = find_piece(p, sched, tile_rows, end - 1, s.total);
+  const int first = end - 1 - x.unit0;                 // the item's first unit
+  if (first < begin || x.unit0 + 1 >= x.units) return;  // another CTA's, or done
+  const int last = s.of(first + x.units - 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mr = warp >> 2, g = warp & 3;
+  const int row = blockIdx.y * kMergeRows + mr, r = x.row0 + row;
+  const int rows = min(sched.n[x.seq], p.max_q) * p.group;
+  if (x.row0 + blockIdx.y * kMergeRows >= rows) return;
+  const size_t stride = (size_t)tile_rows * (D + 2);
+  // the item is its first CTA's second piece unless it starts with the share;
+  // every later CTA's first piece
+  auto part_of = [&](int c) { return p.partial + (2 * c + (c == (int)blockIdx.x && begin < first ? 1 : 0)) * stride; };
+  float top = kNegInf, sum = 0.f, acc[CPL];
 #pragma unroll
-  for (int j = 0; j < CPT; ++j) acc[j] = 0.f;
-  for (int c = blockIdx.x; c <= last; ++c) {
+  for (int j = 0; j < CPL; ++j) acc[j] = 0.f;
+  for (int c = blockIdx.x + lane; c <= last; c += 32) top = fmaxf(top, part_of(c)[tile_rows * D + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll 4
+  for (int c = blockIdx.x + g; c <= last; c += 4) {
     const float* part = part_of(c);
-    const float m = part[tile_rows * D + row];
-    if (m == kNegInf) continue;
-    const float f = ex2(m - top);
-    sum = fmaf(part[tile_rows * D + tile_rows + row], f, sum);
+    const float m = part[tile_rows * D + row], l = part[tile_rows * D + tile_rows + row];
+    float v[CPL];
+    if constexpr (CPL == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(part + row * D + lane * 2);
+    const float f = m == kNegInf ? 0.f : ex2(m - top);
+    sum = fmaf(l, f, sum);
 #pragma unroll
-    for (int j = 0; j < CPT; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(part + row * D + c0 + j);
-      acc[j] = fmaf(v.x, f, acc[j]);
-      acc[j + 1] = fmaf(v.y, f, acc[j + 1]);
-      acc[j + 2] = fmaf(v.z, f, acc[j + 2]);
-      acc[j + 3] = fmaf(v.w, f, acc[j + 3]);
-    }
+    for (int j = 0; j < CPL; ++j) acc[j] = fmaf(v[j], f, acc[j]);
   }
-  const size_t tk = x.tok0 + r / p.group;
-  const int h = x.head * p.group + r % p.group;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat162 v[CPT / 2];
 #pragma unroll
-  for (int j = 0; j < CPT / 2; ++j) v[j] = __floats2bfloat162_rn(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-  __nv_bfloat16* dst = p.out + tk * p.ldo + h * D + c0;
-  if constexpr (CPT == 8) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(v);
-  else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(v);
-  if (p.lse != nullptr && c0 == 0)
+  for (int j = 0; j < CPL; ++j) acc_s[mr][g][lane * CPL + j] = acc[j];
+  if (lane == 0) sum_s[mr][g] = sum;
+  __syncthreads();
+  if (g != 0 || r >= rows) return;
+  sum = (sum_s[mr][0] + sum_s[mr][1]) + (sum_s[mr][2] + sum_s[mr][3]);
+  const int tok = r / p.group;
+  const size_t tk = sched.tok0[x.seq] + tok;
+  const int h = x.head * p.group + r - tok * p.group;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat162 v[CPL / 2];
+#pragma unroll
+  for (int j = 0; j < CPL; ++j) {
+    const int c = lane * CPL + j;
+    acc[j] = ((acc_s[mr][0][c] + acc_s[mr][1][c]) + (acc_s[mr][2][c] + acc_s[mr][3][c])) * inv;
+  }
+#pragma unroll
+  for (int j = 0; j < CPL / 2; ++j) v[j] = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
+  __nv_bfloat16* dst = p.out + tk * p.ldo + h * D + lane * CPL;
+  if constexpr (CPL == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(v);
+  else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(v);
+  if (p.lse != nullptr && lane == 0)
     p.lse[tk * p.q_heads + h] = sum == 0.f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
@@ -553,7 +576,7 @@ cudaError_t launch_tile(const AttendParams& p, const uint8_t* k, const uint8_t* 
 template <int D>
 cudaError_t launch_merge(const AttendParams& p, int tile_rows, int unit, int ctas, cudaStream_t st, bool pdl) {
   void* args[] = {(void*)&p, (void*)&tile_rows, (void*)&unit};
-  return launch_pdl((const void*)qg_attend_merge_kernel<D>, dim3(ctas, tile_rows / 16), 256, 0, args, st, pdl);
+  return launch_pdl((const void*)qg_attend_merge_kernel<D>, dim3(ctas, tile_rows / kMergeRows), kMergeRows * 128, 0, args, st, pdl);
 }
 
 }  // namespace

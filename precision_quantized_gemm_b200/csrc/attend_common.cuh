@@ -71,110 +71,103 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) 
 // equal contiguous shares, so ragged lengths balance without a host copy.  An
 // item that spans CTAs leaves one partial (o, m, l) per CTA, which a second
 // kernel merges in CTA order: the same inputs give the same bits.
+// All counts are 32-bit (the host bounds the units).
+struct Sched {
+  int pre[kAttendMaxBatch + 1];   // units of the sequences before b; [batch]: all
+  int tok0[kAttendMaxBatch];      // first token in q
+  int n[kAttendMaxBatch];         // tokens
+  int len[kAttendMaxBatch];       // cached positions
+  int warp_tot[32];
+};
 struct Share {
-  long long total, begin, end;  // units
-  int ctas;                     // CTAs with work
+  int total, quota, extra, ctas;  // units; the first `extra` CTAs take quota + 1
+  __device__ __forceinline__ int begin(int c) const { return c * quota + min(c, extra); }
+  // The CTA whose share holds unit u.
+  __device__ __forceinline__ int of(int u) const {
+    const int wide = extra * (quota + 1);
+    return u < wide ? (int)((unsigned)u / (unsigned)(quota + 1)) : extra + (int)((unsigned)(u - wide) / (unsigned)quota);
+  }
 };
 
-__device__ __forceinline__ int seq_tokens(const AttendParams& p, int b) {
-  const int a = min(max(__ldg(p.q_offsets + b), 0), p.tokens);
-  const int e = min(max(__ldg(p.q_offsets + b + 1), 0), p.tokens);
-  return max(e - a, 0);
-}
-__device__ __forceinline__ int seq_len(const AttendParams& p, int b) {
-  // the table's row covers ldp pages
-  const long long cap = (long long)p.ldp << p.page_shift;
-  return (int)min((long long)max(__ldg(p.kv_len + b), 0), cap);
-}
-__device__ __forceinline__ int seq_row_tiles(const AttendParams& p, int n, int tile_rows) {
-  return (min(n, p.max_q) * p.group + tile_rows - 1) / tile_rows;
-}
-// a sequence without cached positions still has rows to write (zeros)
-__device__ __forceinline__ int seq_units(int len, int unit) { return max((len + unit - 1) / unit, 1); }
-
-// pre[b] = units of the sequences before b, pre[batch] = all units.  Every
-// thread of the CTA calls it (blockDim.x a multiple of 32, up to 1024).
-__device__ __forceinline__ void scan_units(const AttendParams& p, int tile_rows, int unit, long long* pre,
-                                           long long* warp_tot) {
+// Every thread of the CTA calls it (blockDim.x a multiple of 32, up to 1024);
+// ends with a barrier.
+__device__ __forceinline__ Share plan_units(const AttendParams& p, int tile_rows, int unit, Sched& s) {
   const int per = (p.batch + blockDim.x - 1) / blockDim.x;
-  const int b0 = threadIdx.x * per;
-  long long sum = 0;
-  for (int b = b0; b < min(b0 + per, p.batch); ++b) {
-    const int rt = seq_row_tiles(p, seq_tokens(p, b), tile_rows);
-    const long long u = rt ? (long long)rt * p.kv_heads * seq_units(seq_len(p, b), unit) : 0;
-    pre[b + 1] = u;
+  const int b0 = threadIdx.x * per, b1 = min(b0 + per, p.batch);
+  int sum = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int a = min(max(__ldg(p.q_offsets + b), 0), p.tokens);
+    const int n = max(min(max(__ldg(p.q_offsets + b + 1), 0), p.tokens) - a, 0);
+    // the table's row covers ldp pages
+    const int len = min(max(__ldg(p.kv_len + b), 0), p.ldp << p.page_shift);
+    s.tok0[b] = a;
+    s.n[b] = n;
+    s.len[b] = len;
+    const int tiles = (min(n, p.max_q) * p.group + tile_rows - 1) / tile_rows;
+    // a sequence without cached positions still has rows to write (zeros)
+    const int u = tiles * p.kv_heads * max((len + unit - 1) / unit, 1);
+    s.pre[b + 1] = u;
     sum += u;
   }
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  long long inc = sum;
+  int inc = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+    const int o = __shfl_up_sync(0xffffffffu, inc, d);
     if (l >= d) inc += o;
   }
-  if (l == 31) warp_tot[w] = inc;
+  if (l == 31) s.warp_tot[w] = inc;
   __syncthreads();
-  long long run = inc - sum;
-  for (int j = 0; j < w; ++j) run += warp_tot[j];
-  for (int b = b0; b < min(b0 + per, p.batch); ++b) {
-    run += pre[b + 1];
-    pre[b + 1] = run;
+  int run = inc - sum;
+#pragma unroll 1
+  for (int j = 0; j < w; ++j) run += s.warp_tot[j];
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    run += s.pre[b + 1];
+    s.pre[b + 1] = run;
   }
-  if (threadIdx.x == 0) pre[0] = 0;
+  if (threadIdx.x == 0) s.pre[0] = 0;
   __syncthreads();
-}
-__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) { return total * c / ctas; }
-// The CTA whose share holds unit u.
-__device__ __forceinline__ int share_of(long long total, int ctas, long long u) {
-  return (int)(((u + 1) * ctas - 1) / total);
-}
-__device__ __forceinline__ Share my_share(const AttendParams& p, const long long* pre, int ctas_max, int c) {
-  Share s;
-  s.total = pre[p.batch];
-  s.ctas = (int)min((long long)ctas_max, s.total);
-  s.begin = c < s.ctas ? share_begin(s.total, s.ctas, c) : 0;
-  s.end = c < s.ctas ? share_begin(s.total, s.ctas, c + 1) : 0;
-  return s;
+  Share x;
+  x.total = s.pre[p.batch];
+  x.ctas = max(min((int)gridDim.x, x.total), 1);
+  x.quota = (unsigned)x.total / (unsigned)x.ctas;
+  x.extra = x.total - x.quota * x.ctas;
+  return x;
 }
 
-// One CTA's part of one item.
+// One CTA's part of one item: units [unit0, unit1) of its `units`.
 struct Piece {
-  int seq, head, row0;       // sequence, key head, first row
-  int tok0, n, len;          // first token in q, tokens, cached positions
-  int rows;                  // rows of the sequence (tokens within max_q x group)
-  int unit0, unit1, units;   // units [unit0, unit1) of the item's `units`
+  int seq, head, row0, unit0, unit1, units;
 };
-__device__ __forceinline__ Piece find_piece(const AttendParams& p, const long long* pre, int tile_rows, int unit,
-                                            long long u, long long end) {
+__device__ __forceinline__ Piece find_piece(const AttendParams& p, const Sched& s, int tile_rows, int u, int end) {
   int lo = 0, hi = p.batch - 1;  // the last sequence with pre[b] <= u
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= u) lo = mid;
+    if (s.pre[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
   Piece x;
   x.seq = lo;
-  x.n = seq_tokens(p, lo);
-  x.len = seq_len(p, lo);
-  x.tok0 = min(max(__ldg(p.q_offsets + lo), 0), p.tokens);
-  x.rows = min(x.n, p.max_q) * p.group;
-  const int rt = seq_row_tiles(p, x.n, tile_rows);
-  x.units = seq_units(x.len, unit);
-  const long long r = u - pre[lo];
-  const int item = (int)(r / x.units);
-  x.unit0 = (int)(r % x.units);
-  x.unit1 = (int)min((long long)x.units, x.unit0 + (end - u));
-  x.head = item / rt;
-  x.row0 = (item % rt) * tile_rows;
+  const int tiles = (min(s.n[lo], p.max_q) * p.group + tile_rows - 1) / tile_rows;
+  x.units = (unsigned)(s.pre[lo + 1] - s.pre[lo]) / (unsigned)(tiles * p.kv_heads);
+  const int r = u - s.pre[lo];
+  const int item = (unsigned)r / (unsigned)x.units;
+  x.unit0 = r - item * x.units;
+  x.unit1 = min(x.units, x.unit0 + (end - u));
+  x.head = (unsigned)item / (unsigned)tiles;
+  x.row0 = (item - x.head * tiles) * tile_rows;
   return x;
 }
 
-// Which of the 64 positions from `pos0` on token i of a sequence sees, as bits:
-// the positions before the drafted ones, and the drafted tokens of its mask
-// row, up to `end`.  (i < 0: a row past the last, nothing.)
-__device__ __forceinline__ unsigned long long seen_bits(const AttendParams& p, int tok0, int i, int pos0, int past,
-                                                        int end) {
-  const int count = end - pos0, before = past - pos0;  // positions in range; those before the drafted ones
+// Which of 64 positions token i of a sequence sees, as bits: of the first
+// `count`, the `before` that precede the drafted tokens (negative: the first
+// is drafted token -before), and the drafted ones of its mask row.  (i < 0: a
+// row past the last, nothing.)
+__device__ __forceinline__ unsigned long long seen_bits(const AttendParams& p, int tok0, int i, int count,
+                                                        int before) {
   if (i < 0 || count <= 0) return 0ull;
   const unsigned long long all = count >= 64 ? ~0ull : (1ull << count) - 1;
   if (before >= 64) return all;

@@ -13,8 +13,14 @@
 //   8-11  decode: codes from global memory to f16 in the swizzled operand
 //         tiles, the next tile's codes in registers meanwhile
 //   12    MMA: one thread issues S of tile j + 1 before O of tile j
-//   13    scales of the tiles ahead (log2 and reciprocal once per position),
-//         and the prefetch of their codes into L2
+//   13    the tiles ahead: where their positions lie, what of them counts,
+//         their scales (log2 and reciprocal once per position), and the
+//         prefetch of their codes into L2
+// Only warp 13 walks sequences, heads and pages; the others read its tile
+// descriptors.  That is for the instruction cache: five roles' loops share
+// it, and with a walk inlined into each the warps waited for instructions
+// five times as long as they issued (350 us against TIMING for 8 trees of
+// 32-64 tokens, 64 query and 8 key heads, 2048-8192 positions).
 //
 // What bounds it: per tile the two MMAs are 1024 tensor cycles, the 16384
 // exponentials 1024 cycles of the 16-wide unit, and shared memory carries the
@@ -32,14 +38,24 @@ namespace qg {
 constexpr int kTileRows = 128;
 constexpr int kTilePos = 128;       // positions per tile = unit of work
 constexpr int kTileThreads = 512;
-constexpr int kScaleStages = 4;
+constexpr int kTileStages = 6;     // descriptors and scales ahead
 constexpr float kRescaleAt = 8.f;   // log2
 
 template <int D>
 struct TileSmem {
   static constexpr int kOperand = kTilePos * D * 2;    // f16 tile of K or V
   static constexpr int kScales = 3 * kTilePos * 4;     // key scale, log2 vs, 1 / vs
-  static constexpr int kTotal = 1024 + 4 * kOperand + kScaleStages * kScales;
+  static constexpr int kTotal = 1024 + 4 * kOperand + kTileStages * kScales;
+};
+// What a tile is; written by warp 13.
+struct TileDesc {
+  int run[kTilePos / 16];  // cache row of the 1st of each 16 positions
+  int count;               // positions of the sequence from the tile's first on (may pass 128)
+  int before;              // those before the drafted tokens (may be negative)
+  int first, last;         // of its piece
+  int whole;               // the piece is the whole item
+  int row0, rows;          // first row, rows of the sequence
+  int tok0, head, slot;    // slot: partial result, when not whole
 };
 // TMEM columns
 constexpr int kTmemS = 0;        // two score tiles of 128
@@ -114,48 +130,23 @@ __device__ __forceinline__ void lds_2u64(uint32_t a, uint64_t& x, uint64_t& y) {
 // Barrier of the 64 threads of warps w and w ^ 4 (ids 1 .. 4).
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id + 1) : "memory"); }
 
-// The tiles of a CTA's share, piece after piece.
-struct TileWalk {
-  Piece x;
-  long long u, end;
-  int tile;          // tile of the piece
-  bool live;
-  __device__ __forceinline__ void start(const AttendParams& p, const long long* pre, const Share& s) {
-    u = s.begin;
-    end = s.end;
-    live = u < end;
-    if (live) open(p, pre);
-  }
-  __device__ __forceinline__ void open(const AttendParams& p, const long long* pre) {
-    x = find_piece(p, pre, kTileRows, kTilePos, u, end);
-    tile = x.unit0;
-  }
-  __device__ __forceinline__ bool first() const { return tile == x.unit0; }
-  __device__ __forceinline__ bool last() const { return tile + 1 == x.unit1; }
-  __device__ __forceinline__ void next(const AttendParams& p, const long long* pre) {
-    ++u;
-    if (u >= end) live = false;
-    else if (last()) open(p, pre);
-    else ++tile;
-  }
-};
-
 template <int D, bool INT8>
 __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const uint8_t* __restrict__ k_codes,
                                                                           const uint8_t* __restrict__ v_codes,
                                                                           const AttendParams p) {
   using S = TileSmem<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long pre[kAttendMaxBatch + 1];
-  __shared__ long long warp_tot[kTileThreads / 32];
+  __shared__ Sched sched;
+  __shared__ TileDesc descs[kTileStages];
   // full: the operand tile is decoded / the scores, weights, queries are in
   // TMEM; free: its reader is done (s_full also frees K's buffer, o_done the
   // weights').  No barrier can complete two phases past one of its waiters:
   // each next phase needs what that waiter does after the wait.
   __shared__ __align__(8) uint64_t k_full[2], v_full[2], v_free[2], s_full[2], s_free[2], w_full, o_done, q_full, idle,
-      sc_full[kScaleStages], sc_free[kScaleStages];
+      d_full[kTileStages], d_free[kTileStages];
   __shared__ uint32_t tmem_ptr;
-  __shared__ float swap[2][kTileRows];
+  __shared__ float swap_a[2][kTileRows], swap_m[2][kTileRows], swap_l[2][kTileRows];  // between partners
+  __shared__ bool pair_ok[2][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
   const uint32_t k_tile = base, v_tile = base + 2 * S::kOperand, scales = base + 4 * S::kOperand;
@@ -171,9 +162,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
     mbar_init(&o_done, 1);
     mbar_init(&q_full, 8);
     mbar_init(&idle, 1);
-    for (int i = 0; i < kScaleStages; ++i) {
-      mbar_init(&sc_full[i], 1);
-      mbar_init(&sc_free[i], 8);
+    for (int i = 0; i < kTileStages; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_free[i], 13);  // softmax, decode and MMA warps
     }
     fence_barrier_init();
   }
@@ -183,10 +174,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
   }
   griddep_launch_dependents();
   griddep_wait();
-  scan_units(p, kTileRows, kTilePos, pre, warp_tot);  // also orders the barriers' and tmem_ptr's set-up
+  const Share share = plan_units(p, kTileRows, kTilePos, sched);  // also orders the barriers' set-up
   tc_fence_after();
   const uint32_t tmem = tmem_ptr;
-  const Share share = my_share(p, pre, gridDim.x, blockIdx.x);
+  const bool works = (int)blockIdx.x < share.ctas && share.total > 0;
+  const int u0 = works ? share.begin(blockIdx.x) : 0, u1 = works ? share.begin(blockIdx.x + 1) : 0;
+  const int tiles = u1 - u0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = mbar_wait(bar, parity, p.err, p.wait_ns);
@@ -202,18 +195,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
     uint64_t l2 = 0;
     int tok = -1;
     bool live_warp = false;
-    TileWalk w;
-    w.start(p, pre, share);
-    for (int j = 0; w.live; ++j, w.next(p, pre)) {
-      const Piece& x = w.x;
-      const int r = x.row0 + row;
-      if (w.first()) {
+    int st = 0;
+    uint32_t ring = 0;  // parity of the descriptors' turn
+    // Partners agree on whether the next descriptor is there: what it says
+    // decides which of the pair's barriers they meet at.  (The barrier also
+    // ends the turn's use of swap_m.)
+    auto open = [&]() {
+      wait(&d_full[st], ring);
+      __syncwarp();
+      if (lane == 0) pair_ok[half][warp & 3] = ok;
+      pair_sync(warp & 3);
+      return pair_ok[0][warp & 3] && pair_ok[1][warp & 3];
+    };
+    bool have = tiles > 0 && open();
+#pragma unroll 1
+    for (int j = 0; j < tiles && have; ++j) {
+      const TileDesc& x = descs[st];
+      const bool first = x.first, last = x.last;
+      if (first) {
         // queries: f16, the row's largest magnitude brought to [2^14, 2^15);
         // this thread's half of the channels
+        const int r = x.row0 + row;
         live_warp = x.row0 + (warp & 3) * 32 < x.rows;
         tok = r < x.rows ? r / p.group : -1;
         const __nv_bfloat16* src =
-            tok < 0 ? nullptr : p.q + (size_t)(x.tok0 + tok) * p.ldq + (x.head * p.group + r % p.group) * D + half * (D / 2);
+            tok < 0 ? nullptr
+                    : p.q + (size_t)(x.tok0 + tok) * p.ldq + (x.head * p.group + r - tok * p.group) * D + half * (D / 2);
         uint32_t q[D / 4];
         float amax = 0.f;
 #pragma unroll
@@ -227,9 +234,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
 #pragma unroll
         for (int c = 0; c < D / 4; ++c)
           amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(q[c] << 16)), fabsf(__uint_as_float(q[c] & 0xffff0000u))));
-        swap[half][row] = amax;
+        swap_a[half][row] = amax;
         pair_sync(warp & 3);
-        amax = fmaxf(amax, swap[half ^ 1][row]);
+        amax = fmaxf(amax, swap_a[half ^ 1][row]);
         float up, down;
         row_power(amax, up, down);
         power = down * p.scale_log2;
@@ -246,13 +253,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
         if (lane == 0) mbar_arrive(&q_full);
         m = kNegInf;
         l2 = 0;
-        pair_sync(warp & 3);  // swap is free again
       }
-      const int pos0 = w.tile * kTilePos, past = x.len - x.n;
-      const int st = j % kScaleStages;
       const uint32_t sc = scales + st * S::kScales + half * 64 * 4;
       wait(&s_full[j & 1], (j >> 1) & 1);
-      wait(&sc_full[st], (j / kScaleStages) & 1);
       float t[64];
       float top = kNegInf;
       if (live_warp && __all_sync(0xffffffffu, ok)) {
@@ -275,8 +278,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
           unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(t[i], t[i + 1]), pw), ka, va), t[i], t[i + 1]);
           unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(t[i + 2], t[i + 3]), pw), kb, vb), t[i + 2], t[i + 3]);
         }
-        if (pos0 + kTilePos > past) {
-          const unsigned long long see = seen_bits(p, x.tok0, tok, pos0 + half * 64, past, x.len);
+        if (x.before < kTilePos || x.count < kTilePos) {
+          const unsigned long long see = seen_bits(p, x.tok0, tok, x.count - half * 64, x.before - half * 64);
           const uint32_t see_lo = (uint32_t)see, see_hi = (uint32_t)(see >> 32);
 #pragma unroll
           for (int i = 0; i < 64; ++i)
@@ -288,9 +291,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[j & 1]);
-      swap[half][row] = top;
+      swap_m[half][row] = top;
       pair_sync(warp & 3);
-      top = fmaxf(top, swap[half ^ 1][row]);
+      top = fmaxf(top, swap_m[half ^ 1][row]);
       const bool grown = top > m + kRescaleAt || (m == kNegInf && top > kNegInf);
       // the accumulator, the weights' columns and (below) the sums follow the
       // previous tile's product
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
           const float f = grown ? ex2(m - top) : 1.f;
           if (grown) m = top;
           l2 = mul_f32x2(l2, pack_f32x2(f, f));
-          if (!w.first()) {
+          if (!first) {
 #pragma unroll
             for (int c = 0; c < OC; c += 32) {
               uint32_t o[32];
@@ -331,31 +334,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&w_full);
-        mbar_arrive(&sc_free[st]);
-      }
-      pair_sync(warp & 3);  // swap is free again
+      if (lane == 0) mbar_arrive(&w_full);
 
-      if (w.last()) {
+      if (last) {
         // the item's (or this part's) result
         float la, lb;
         unpack_f32x2(l2, la, lb);
         float l = la + lb;
-        swap[half][row] = l;
+        swap_l[half][row] = l;
         pair_sync(warp & 3);
-        l += swap[half ^ 1][row];
+        l += swap_l[half ^ 1][row];
         if (l != l) m = 0.f;  // a NaN row keeps its place in the merge
         wait(&o_done, j & 1);
         if (live_warp && __all_sync(0xffffffffu, ok)) {
           tc_fence_after();
-          const bool whole = x.unit0 == 0 && x.unit1 == x.units;
-          const bool write = r < x.rows;
-          const int slot = 2 * blockIdx.x + (w.u + 1 - (x.unit1 - x.unit0) == share.begin ? 0 : 1);
-          float* part = p.partial + (size_t)slot * kTileRows * (D + 2);
+          const bool whole = x.whole, write = tok >= 0;
+          const int r = x.row0 + row;
+          float* part = p.partial + (size_t)x.slot * kTileRows * (D + 2);
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const size_t tk = write ? x.tok0 + tok : 0;
-          const int h = write ? x.head * p.group + r % p.group : 0;
+          const int h = write ? x.head * p.group + r - tok * p.group : 0;
 #pragma unroll
           for (int c = 0; c < OC; c += 32) {
             uint32_t o[32];
@@ -390,8 +388,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
           }
           tc_fence_before();
         }
-        pair_sync(warp & 3);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_free[st]);
+      if (++st == kTileStages) st = 0, ring ^= 1;
+      if (j + 1 < tiles) have = open();
     }
   } else if (warp < 12) {
     // -------------------------------------------------------------- decode --
@@ -402,25 +403,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
     constexpr int N = 32 / RPI;               // instructions per warp and tile
     const int c = D == 128 ? (lane & 3) + ((lane >> 4) << 2) : lane & 3;
     const int r0 = (warp - 8) * 32 + (D == 128 ? (lane >> 2) & 3 : lane >> 2);
-    auto load = [&](const TileWalk& w, const uint8_t* codes, uint4 (&buf)[N]) {
-      if (!w.live) return;
-      const int* table = p.table + (size_t)w.x.seq * p.ldp;
-      const int pos0 = w.tile * kTilePos + r0;
-      int page[2];  // of the warp's first and second 16 positions
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = w.tile * kTilePos + (warp - 8) * 32 + i * 16;
-        page[i] = at < w.x.len ? min(max(__ldg(table + (at >> p.page_shift)), 0), p.pages - 1) : 0;
-      }
+    auto load = [&](int j, const uint8_t* codes, uint4 (&buf)[N], bool done) {
+      const int st = j % kTileStages;
+      wait(&d_full[st], (j / kTileStages) & 1);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const TileDesc& x = descs[st];
+      const int run[2] = {x.run[(warp - 8) * 2], x.run[(warp - 8) * 2 + 1]};
+      const int count = x.count - r0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int pos = pos0 + i * RPI;
         buf[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (pos < w.x.len) {
-          const size_t rr = ((size_t)page[i / (N / 2)] * p.kv_heads + w.x.head << p.page_shift) +
-                            (pos & ((1 << p.page_shift) - 1));
-          buf[i] = __ldg(reinterpret_cast<const uint4*>(codes + rr * D) + c);
-        }
+        if (i * RPI < count)
+          buf[i] = __ldg(reinterpret_cast<const uint4*>(
+                             codes + (size_t)(run[i / (N / 2)] + (r0 & 15) + i % (N / 2) * RPI) * D) + c);
+      }
+      if (done) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_free[st]);
       }
     };
     auto store = [&](uint32_t tile, const uint4 (&buf)[N]) {
@@ -442,45 +441,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       fence_proxy_async_smem();
       __syncwarp();
     };
-    uint4 kb[N], vb[N];
-    TileWalk wk, wv;
-    wk.start(p, pre, share);
-    wv = wk;
-    load(wk, k_codes, kb);
-    if (wk.live) {
-      store(k_tile, kb);
-      if (lane == 0) mbar_arrive(&k_full[0]);
-      wk.next(p, pre);
-      load(wk, k_codes, kb);
-      load(wv, v_codes, vb);
-    }
-    for (int j = 0; wv.live; ++j) {
-      if (wk.live) {
-        const int i = j + 1;
+    uint4 kb[N] = {}, vb[N] = {};
+    if (tiles > 0) load(0, k_codes, kb, false);
+    // turn j: K of tile j + 1, then V of tile j (turn -1: only K)
+#pragma unroll 1
+    for (int j = -1; j < tiles; ++j) {
+      const int i = j + 1;
+      if (i < tiles) {
         if (i >= 2) wait(&s_full[i & 1], ((i - 2) >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         store(k_tile + (i & 1) * S::kOperand, kb);
         if (lane == 0) mbar_arrive(&k_full[i & 1]);
-        wk.next(p, pre);
-        load(wk, k_codes, kb);
+        if (i + 1 < tiles) load(i + 1, k_codes, kb, false);
       }
-      if (j >= 2) wait(&v_free[j & 1], ((j - 2) >> 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      store(v_tile + (j & 1) * S::kOperand, vb);
-      if (lane == 0) mbar_arrive(&v_full[j & 1]);
-      wv.next(p, pre);
-      load(wv, v_codes, vb);
+      if (j >= 0) {
+        if (j >= 2) wait(&v_free[j & 1], ((j - 2) >> 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        store(v_tile + (j & 1) * S::kOperand, vb);
+        if (lane == 0) mbar_arrive(&v_full[j & 1]);
+      }
+      if (i < tiles) load(i, v_codes, vb, true);
     }
   } else if (warp == 12) {
     // ----------------------------------------------------------------- MMA --
     if (lane == 0) {
       const uint64_t kd = sdesc_sw128(k_tile), vd = sdesc_mn_sw128(v_tile, kTilePos * 128);
       int queries = 0;
-      TileWalk wq, wo;
-      wq.start(p, pre, share);
-      wo = wq;
+      bool first = false;  // tile j + 1 is the first of its piece
+      auto look = [&](int j) {
+        const int st = j % kTileStages;
+        if (!wait(&d_full[st], (j / kTileStages) & 1)) return;
+        first = descs[st].first;
+        mbar_arrive(&d_free[st]);
+      };
       auto scores = [&](int j) {
-        if (wq.first() && !wait(&q_full, queries++ & 1)) return;
+        if (first && !wait(&q_full, queries++ & 1)) return;
         if (!wait(&k_full[j & 1], (j >> 1) & 1)) return;
         if (j >= 2 && !wait(&s_free[j & 1], ((j - 2) >> 1) & 1)) return;
         tc_fence_after();
@@ -490,24 +485,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
                      kd + (((j & 1) * S::kOperand + (k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4),
                      idesc_f16(kTilePos, false), k > 0);
         mma_commit(&s_full[j & 1]);
-        wq.next(p, pre);
       };
-      for (int j = 0; wo.live && ok; ++j) {
-        if (j == 0) scores(0);
-        // the next piece's first scores need its queries, which wait for this
-        // piece's last product
-        const bool ahead = wq.live && !wq.first();
-        if (ok && ahead) scores(j + 1);
-        if (!ok || !wait(&w_full, j & 1) || !wait(&v_full[j & 1], (j >> 1) & 1)) break;
-        tc_fence_after();
+      // turn j: scores of tile j + 1, then the product of tile j; the other
+      // way round where a piece starts: its first scores need its queries,
+      // which wait for the last piece's last product
+#pragma unroll 1
+      for (int j = -1; j < tiles && ok; ++j) {
+        const bool start = j >= 0 && first;  // tile j opens its piece
+        if (j + 1 < tiles) look(j + 1);
+        else first = false;
+#pragma unroll 1
+        for (int part = 0; part < 2 && ok; ++part) {
+          if ((part == 1) == first) {
+            if (j + 1 < tiles) scores(j + 1);
+          } else if (j >= 0) {
+            if (!wait(&w_full, j & 1) || !wait(&v_full[j & 1], (j >> 1) & 1)) break;
+            tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kTilePos / 16; ++k)
-          mma_f16_ts(tmem + kTmemO, tmem + kTmemW + 8 * k, vd + (((j & 1) * S::kOperand + k * 2048) >> 4),
-                     idesc_f16(D, true), !wo.first() || k > 0);
-        mma_commit(&o_done);
-        mma_commit(&v_free[j & 1]);
-        if (!ahead && wq.live) scores(j + 1);
-        wo.next(p, pre);
+            for (int k = 0; k < kTilePos / 16; ++k)
+              mma_f16_ts(tmem + kTmemO, tmem + kTmemW + 8 * k, vd + (((j & 1) * S::kOperand + k * 2048) >> 4),
+                         idesc_f16(D, true), !start || k > 0);
+            mma_commit(&o_done);
+            mma_commit(&v_free[j & 1]);
+          }
+        }
       }
       // MMAs still in flight (a wait ran out) end before TMEM is given up
       mma_commit(&idle);
@@ -516,41 +517,83 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
     __syncwarp();
   } else if (warp == 13) {
     // ------------------------------------------------- scales and prefetch --
-    TileWalk w;
-    w.start(p, pre, share);
-    for (int j = 0; w.live && ok; ++j, w.next(p, pre)) {
-      const int st = j % kScaleStages;
-      const int* table = p.table + (size_t)w.x.seq * p.ldp;
-      const int pos0 = w.tile * kTilePos;
-      float ks[4], vs[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int pos = pos0 + i * 32 + lane;
-        ks[i] = vs[i] = 1.f;
-        if (pos < w.x.len) {
-          const int page = min(max(__ldg(table + (pos >> p.page_shift)), 0), p.pages - 1);
-          const size_t row = ((size_t)page * p.kv_heads + w.x.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-          ks[i] = __ldg(p.k_scale + row);
-          vs[i] = __ldg(p.v_scale + row);
-          if ((pos & 15) == 0) {  // 16 positions lie within a page
-            bulk_prefetch_l2(k_codes + row * D, 16 * D);
-            bulk_prefetch_l2(v_codes + row * D, 16 * D);
-          }
+    // A turn loads what tile j + 1 needs before it hands over tile j.  Lane i
+    // has positions 4 i .. 4 i + 3: within one run of 16, whose row its first
+    // lane hands on.
+    Piece x = {};
+    int tile = 0, len = 0;
+    auto step = [&](int j) {
+      if (j == 0 || tile + 1 == x.unit1) {
+        x = find_piece(p, sched, kTileRows, u0 + j, u1);
+        tile = x.unit0;
+        len = sched.len[x.seq];
+      } else {
+        ++tile;
+      }
+    };
+    int row = 0, count = 0;
+    float4 ks = {}, vs = {};
+    auto fetch = [&]() {
+      count = len - tile * kTilePos;
+      row = 0;
+      ks = vs = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (lane * 4 < count) {
+        const int pos = tile * kTilePos + lane * 4;
+        const int page = min(max(__ldg(p.table + (size_t)x.seq * p.ldp + (pos >> p.page_shift)), 0), p.pages - 1);
+        row = (page * p.kv_heads + x.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+        ks = __ldg(reinterpret_cast<const float4*>(p.k_scale + row));
+        vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + row));
+        if ((lane & 3) == 0) {
+          bulk_prefetch_l2(k_codes + (size_t)row * D, 16 * D);
+          bulk_prefetch_l2(v_codes + (size_t)row * D, 16 * D);
         }
       }
-      if (j >= kScaleStages && !wait(&sc_free[st], ((j / kScaleStages) - 1) & 1)) break;
-      const uint32_t sc = scales + st * S::kScales;
+    };
+    if (tiles > 0) {
+      step(0);
+      fetch();
+    }
+    int st = 0;
+    uint32_t ring = 1;
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j) {
+      if (j >= kTileStages) wait(&d_free[st], ring);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      TileDesc& d = descs[st];
+      if ((lane & 3) == 0) d.run[lane >> 2] = row;
+      if (lane == 0) {
+        d.count = count;
+        d.before = count - sched.n[x.seq];
+        d.first = j == 0 || tile == x.unit0;
+        d.last = tile + 1 == x.unit1;
+        d.whole = x.unit0 == 0 && x.unit1 == x.units;
+        d.row0 = x.row0;
+        d.rows = min(sched.n[x.seq], p.max_q) * p.group;
+        d.tok0 = sched.tok0[x.seq];
+        d.head = x.head;
+        d.slot = 2 * blockIdx.x + (j == tile - x.unit0 ? 0 : 1);  // the share's first piece or a later one
+      }
+      const uint32_t at = scales + st * S::kScales + lane * 16;
+      const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {vs.x, vs.y, vs.z, vs.w};
+      float a[4], b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float a, b;
-        value_scale(vs[i], a, b);
-        const uint32_t at = sc + (i * 32 + lane) * 4;
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ks[i]) : "memory");
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + kTilePos * 4), "f"(a) : "memory");
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 2 * kTilePos * 4), "f"(b) : "memory");
+      for (int i = 0; i < 4; ++i) value_scale(v4[i], a[i], b[i]);
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(k4[0]), "f"(k4[1]), "f"(k4[2]),
+                   "f"(k4[3])
+                   : "memory");
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + kTilePos * 4), "f"(a[0]), "f"(a[1]),
+                   "f"(a[2]), "f"(a[3])
+                   : "memory");
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 2 * kTilePos * 4), "f"(b[0]), "f"(b[1]),
+                   "f"(b[2]), "f"(b[3])
+                   : "memory");
+      if (j + 1 < tiles) {
+        step(j + 1);
+        fetch();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sc_full[st]);
+      if (lane == 0) mbar_arrive(&d_full[st]);
+      if (++st == kTileStages) st = 0, ring ^= 1;
     }
   }
   tc_fence_before();
