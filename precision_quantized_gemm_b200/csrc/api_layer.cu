@@ -250,7 +250,6 @@ qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, s
   p.mask = reinterpret_cast<const unsigned long long*>(a->tree_mask);
   p.k_scale = c->k_scale;
   p.v_scale = c->v_scale;
-  p.partial = static_cast<float*>(workspace);
   p.ldq = a->ldq;
   p.ldo = a->ldo;
   p.ldp = a->max_pages;
@@ -273,7 +272,7 @@ qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, s
     if (!qg::make_row_tmap(&tk, c->k, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;
     if (!qg::make_row_tmap(&tv, c->v, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;
   }
-  return qg::launch_attend(p, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), &tk, &tv,
+  return qg::launch_attend(p, workspace, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), &tk, &tv,
                            c->head_dim, c->format == QG_W8A8_INT8, st.sms, (cudaStream_t)stream,
                            st.pdl) == cudaSuccess
              ? QG_OK

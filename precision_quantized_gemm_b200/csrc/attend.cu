@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   griddep_launch_dependents();
   griddep_wait();
   const Share share = plan_units(p, kRows, kUnit, sched);
+  if (threadIdx.x == 0) p.records[blockIdx.x] = merge_record(p, sched, share, kRows);
   if (blockIdx.x >= share.ctas || share.total == 0) return;
   const int share_begin = share.begin(blockIdx.x), share_end = share.begin(blockIdx.x + 1);
   uint32_t phase = 0;  // bit i: parity of the ring stage's next wait
@@ -457,43 +458,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 }
 
-// Merge of the items that span CTAs: CTA c takes the item that starts inside
-// share c and goes on past it (at most one), kMergeRows rows per blockIdx.y.
-// A warp takes one row of every fourth part, D / 32 channels a lane; the four
-// warps of a row meet in shared memory.
-constexpr int kMergeRows = 2;
-template <int D>
-__global__ void __launch_bounds__(kMergeRows * 128) qg_attend_merge_kernel(const AttendParams p, int tile_rows,
-                                                                           int unit) {
+// Merge of the items that span CTAs: CTA c takes the one of its record, ROWS
+// rows per blockIdx.y.  WPR warps share a row: each takes every WPR-th part,
+// D / 32 channels a lane; they meet in shared memory.
+template <int D, int ROWS, int WPR>
+__global__ void __launch_bounds__(ROWS * WPR * 32) qg_attend_merge_kernel(const AttendParams p, int tile_rows) {
   constexpr int CPL = D / 32;
-  __shared__ Sched sched;
-  __shared__ float acc_s[kMergeRows][4][D], sum_s[kMergeRows][4];
+  __shared__ float acc_s[ROWS][WPR][D], sum_s[ROWS][WPR];
   griddep_launch_dependents();
   griddep_wait();
-  const Share s = plan_units(p, tile_rows, unit, sched);
-  if (blockIdx.x + 1 >= s.ctas) return;  // nothing goes on past the last share
-  const int begin = s.begin(blockIdx.x), end = s.begin(blockIdx.x + 1);
-  const Piece x = find_piece(p, sched, tile_rows, end - 1, s.total);
-  const int first = end - 1 - x.unit0;                 // the item's first unit
-  if (first < begin || x.unit0 + 1 >= x.units) return;  // another CTA's, or done
-  const int last = s.of(first + x.units - 1);
+  const MergeRecord rec = p.records[blockIdx.x];
+  if (rec.last < 0 || rec.row0 + (int)blockIdx.y * ROWS >= rec.rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mr = warp >> 2, g = warp & 3;
-  const int row = blockIdx.y * kMergeRows + mr, r = x.row0 + row;
-  const int rows = min(sched.n[x.seq], p.max_q) * p.group;
-  if (x.row0 + blockIdx.y * kMergeRows >= rows) return;
+  const int mr = warp / WPR, g = warp % WPR;
+  const int row = blockIdx.y * ROWS + mr, r = rec.row0 + row;
   const size_t stride = (size_t)tile_rows * (D + 2);
-  // the item is its first CTA's second piece unless it starts with the share;
-  // every later CTA's first piece
-  auto part_of = [&](int c) { return p.partial + (2 * c + (c == (int)blockIdx.x && begin < first ? 1 : 0)) * stride; };
+  auto part_of = [&](int c) { return p.partial + (c == (int)blockIdx.x ? rec.slot : 2 * c) * stride; };
   float top = kNegInf, sum = 0.f, acc[CPL];
 #pragma unroll
   for (int j = 0; j < CPL; ++j) acc[j] = 0.f;
-  for (int c = blockIdx.x + lane; c <= last; c += 32) top = fmaxf(top, part_of(c)[tile_rows * D + row]);
+  for (int c = blockIdx.x + lane; c <= rec.last; c += 32) top = fmaxf(top, part_of(c)[tile_rows * D + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll 4
-  for (int c = blockIdx.x + g; c <= last; c += 4) {
+  for (int c = blockIdx.x + g; c <= rec.last; c += WPR) {
     const float* part = part_of(c);
     const float m = part[tile_rows * D + row], l = part[tile_rows * D + tile_rows + row];
     float v[CPL];
@@ -504,24 +492,27 @@ __global__ void __launch_bounds__(kMergeRows * 128) qg_attend_merge_kernel(const
 #pragma unroll
     for (int j = 0; j < CPL; ++j) acc[j] = fmaf(v[j], f, acc[j]);
   }
+  if constexpr (WPR > 1) {
 #pragma unroll
-  for (int j = 0; j < CPL; ++j) acc_s[mr][g][lane * CPL + j] = acc[j];
-  if (lane == 0) sum_s[mr][g] = sum;
-  __syncthreads();
-  if (g != 0 || r >= rows) return;
-  sum = (sum_s[mr][0] + sum_s[mr][1]) + (sum_s[mr][2] + sum_s[mr][3]);
+    for (int j = 0; j < CPL; ++j) acc_s[mr][g][lane * CPL + j] = acc[j];
+    if (lane == 0) sum_s[mr][g] = sum;
+    __syncthreads();
+    if (g != 0) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      sum += sum_s[mr][w];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) acc[j] += acc_s[mr][w][lane * CPL + j];
+    }
+  }
+  if (r >= rec.rows) return;
   const int tok = r / p.group;
-  const size_t tk = sched.tok0[x.seq] + tok;
-  const int h = x.head * p.group + r - tok * p.group;
+  const size_t tk = rec.tok0 + tok;
+  const int h = rec.head * p.group + r - tok * p.group;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   __nv_bfloat162 v[CPL / 2];
 #pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    const int c = lane * CPL + j;
-    acc[j] = ((acc_s[mr][0][c] + acc_s[mr][1][c]) + (acc_s[mr][2][c] + acc_s[mr][3][c])) * inv;
-  }
-#pragma unroll
-  for (int j = 0; j < CPL / 2; ++j) v[j] = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
+  for (int j = 0; j < CPL / 2; ++j) v[j] = __floats2bfloat162_rn(acc[2 * j] * inv, acc[2 * j + 1] * inv);
   __nv_bfloat16* dst = p.out + tk * p.ldo + h * D + lane * CPL;
   if constexpr (CPL == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(v);
   else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(v);
@@ -573,10 +564,15 @@ cudaError_t launch_tile(const AttendParams& p, const uint8_t* k, const uint8_t* 
   return launch_pdl(fn, dim3(ctas), kTileThreads, smem, args, st, pdl);
 }
 
+// The rows kernel may leave an item in a part per SM, of few rows: four warps
+// a row.  The tile kernel's items have up to 128 rows: one warp each.
 template <int D>
-cudaError_t launch_merge(const AttendParams& p, int tile_rows, int unit, int ctas, cudaStream_t st, bool pdl) {
-  void* args[] = {(void*)&p, (void*)&tile_rows, (void*)&unit};
-  return launch_pdl((const void*)qg_attend_merge_kernel<D>, dim3(ctas, tile_rows / kMergeRows), kMergeRows * 128, 0, args, st, pdl);
+cudaError_t launch_merge(const AttendParams& p, bool tiles, int ctas, cudaStream_t st, bool pdl) {
+  int tile_rows = tiles ? kTileRows : kRows;
+  void* args[] = {(void*)&p, (void*)&tile_rows};
+  if (tiles)
+    return launch_pdl((const void*)qg_attend_merge_kernel<D, 16, 1>, dim3(ctas, kTileRows / 16), 512, 0, args, st, pdl);
+  return launch_pdl((const void*)qg_attend_merge_kernel<D, 2, 4>, dim3(ctas, kRows / 2), 256, 0, args, st, pdl);
 }
 
 }  // namespace
@@ -586,12 +582,14 @@ cudaError_t launch_merge(const AttendParams& p, int tile_rows, int unit, int cta
 bool attend_tiles(int rows_max) { return rows_max > kRows; }
 
 size_t attend_workspace(int head_dim, int rows_max, int sms) {
-  return (size_t)2 * sms * (attend_tiles(rows_max) ? kTileRows : kRows) * (head_dim + 2) * 4;
+  return sizeof(MergeRecord) * sms + (size_t)2 * sms * (attend_tiles(rows_max) ? kTileRows : kRows) * (head_dim + 2) * 4;
 }
 
-cudaError_t launch_attend(const AttendParams& p, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
+cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
                           const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl) {
   const bool tiles = attend_tiles(p.max_q * p.group);
+  p.records = static_cast<MergeRecord*>(workspace);
+  p.partial = reinterpret_cast<float*>(p.records + sms);
   cudaError_t e;
   if (tiles) {
     if (head_dim == 128)
@@ -604,9 +602,7 @@ cudaError_t launch_attend(const AttendParams& p, const uint8_t* k, const uint8_t
     e = int8 ? launch_rows<64, true>(p, *tk, *tv, sms, st, pdl) : launch_rows<64, false>(p, *tk, *tv, sms, st, pdl);
   }
   if (e != cudaSuccess) return e;
-  const int rows = tiles ? kTileRows : kRows, unit = tiles ? kTilePos : kUnit;
-  return head_dim == 128 ? launch_merge<128>(p, rows, unit, sms, st, pdl)
-                         : launch_merge<64>(p, rows, unit, sms, st, pdl);
+  return head_dim == 128 ? launch_merge<128>(p, tiles, sms, st, pdl) : launch_merge<64>(p, tiles, sms, st, pdl);
 }
 
 }  // namespace qg

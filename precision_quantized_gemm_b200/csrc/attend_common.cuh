@@ -162,6 +162,33 @@ __device__ __forceinline__ Piece find_piece(const AttendParams& p, const Sched& 
   return x;
 }
 
+// What the merge has to know of an item that starts in a CTA's share and goes
+// on past it (there is at most one): every CTA of the grid leaves one record
+// in the workspace, `last` < 0 for none.  The parts are this CTA's slot and
+// the first slot of each CTA up to `last`.
+struct MergeRecord {
+  int last, slot, row0, rows, tok0, head;
+  int pad[2];
+};
+__device__ __forceinline__ MergeRecord merge_record(const AttendParams& p, const Sched& s, const Share& share,
+                                                    int tile_rows) {
+  MergeRecord r = {};
+  r.last = -1;
+  const int c = blockIdx.x;
+  if (c + 1 >= share.ctas) return r;  // nothing goes on past the last share
+  const int begin = share.begin(c), end = share.begin(c + 1);
+  const Piece x = find_piece(p, s, tile_rows, end - 1, share.total);
+  const int first = end - 1 - x.unit0;  // the item's first unit
+  if (first < begin || x.unit0 + 1 >= x.units) return r;
+  r.last = share.of(first + x.units - 1);
+  r.slot = 2 * c + (first > begin ? 1 : 0);
+  r.row0 = x.row0;
+  r.rows = min(s.n[x.seq], p.max_q) * p.group;
+  r.tok0 = s.tok0[x.seq];
+  r.head = x.head;
+  return r;
+}
+
 // Which of 64 positions token i of a sequence sees, as bits: of the first
 // `count`, the `before` that precede the drafted tokens (negative: the first
 // is drafted token -before), and the drafted ones of its mask row.  (i < 0: a

@@ -6,27 +6,31 @@
 //   O += W V       A = W (TMEM, f16), B = V (shared, f16, MN-major) -> TMEM fp32
 //
 // 16 warps in four roles, joined by mbarriers:
-//   0-7   softmax: warp w owns rows 32 (w % 4) .. + 31 (its TMEM lanes), the
-//         first or the second 64 positions of a tile: a thread holds 64 scores
-//         of one row in registers, agrees on the row's maximum with its
-//         partner in warp w ^ 4, and writes the f16 weights to TMEM
+//   0-7   softmax: warps 0-3 take the even tiles, 4-7 the odd ones, warp w the
+//         rows 32 (w % 4) .. + 31 (its TMEM lanes).  A thread holds the scores
+//         of 4 rows x 32 positions (the 16x256b fragments: one position's
+//         scales serve 4 rows) and writes the f16 weights over them in TMEM.
 //   8-11  decode: codes from global memory to f16 in the swizzled operand
 //         tiles, the next tile's codes in registers meanwhile
 //   12    MMA: one thread issues S of tile j + 1 before O of tile j
-//   13    the tiles ahead: where their positions lie, what of them counts,
-//         their scales (log2 and reciprocal once per position), and the
-//         prefetch of their codes into L2
-// Only warp 13 walks sequences, heads and pages; the others read its tile
-// descriptors.  That is for the instruction cache: five roles' loops share
-// it, and with a walk inlined into each the warps waited for instructions
-// five times as long as they issued (350 us against TIMING for 8 trees of
-// 32-64 tokens, 64 query and 8 key heads, 2048-8192 positions).
+//   13-15 the tiles ahead, in turn: where their positions lie, what of them
+//         counts, their scales (log2 and reciprocal once per position), and
+//         the prefetch of their codes into L2
 //
 // What bounds it: per tile the two MMAs are 1024 tensor cycles, the 16384
 // exponentials 1024 cycles of the 16-wide unit, and shared memory carries the
 // decoded tiles twice (64 KB written, 64 KB read by the MMAs: 1024 cycles).
 // That is why Q and W sit in TMEM (from shared memory they would add 64 KB a
-// tile) and codes do not pass through shared memory on their way to f16.
+// tile), codes do not pass through shared memory on their way to f16, and the
+// scores are read in the fragment layout: with a row per thread every warp
+// would load every position's three scales for 32 lanes (192 KB a tile).
+// One tile's chain (load, scores, maximum, exponentials, store) is several
+// times that long, so two groups of warps work on two tiles at once; only the
+// rows' reference maximum passes from one group to the other.
+// Only warps 13-15 walk sequences, heads and pages; the others read tile
+// descriptors.  That is for the instruction cache, which the roles' loops
+// share: with a walk inlined into each role the warps waited for instructions
+// five times as long as they issued.
 // The accumulator is rescaled only when a row's maximum has grown by more
 // than 2^8 since its reference was taken: weights stay below 256, and sums
 // and accumulator keep the same reference, so the result is unchanged.
@@ -47,23 +51,27 @@ struct TileSmem {
   static constexpr int kScales = 3 * kTilePos * 4;     // key scale, log2 vs, 1 / vs
   static constexpr int kTotal = 1024 + 4 * kOperand + kTileStages * kScales;
 };
-// What a tile is; written by warp 13.
+// The spin of a wait, out of line: the instruction cache holds one copy.
+__device__ __noinline__ bool tile_spin(uint64_t* bar, uint32_t parity, unsigned int* err, unsigned long long limit) {
+  return mbar_wait(bar, parity, err, limit);
+}
+
+// What a tile is; written by warps 13-15.
 struct TileDesc {
   int run[kTilePos / 16];  // cache row of the 1st of each 16 positions
   int count;               // positions of the sequence from the tile's first on (may pass 128)
   int before;              // those before the drafted tokens (may be negative)
-  int first, last;         // of its piece
+  int item;                // its item's first unit
+  int first, last, next_last;  // of its piece; the next tile is its last
   int whole;               // the piece is the whole item
   int row0, rows;          // first row, rows of the sequence
   int tok0, head, slot;    // slot: partial result, when not whole
 };
 // TMEM columns
-constexpr int kTmemS = 0;        // two score tiles of 128
+constexpr int kTmemS = 0;        // two score tiles of 128; their weights over the first 64
 constexpr int kTmemO = 256;      // D
-constexpr int kTmemW = 384;      // 64: 128 f16 weights
-constexpr int kTmemQ = 448;      // D / 2
+constexpr int kTmemQ = 384;      // D / 2
 constexpr int kTmemCols = 512;
-
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
   return (1u << 4)                            // D = f32; A, B = f16
          | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -116,6 +124,11 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
@@ -124,11 +137,26 @@ __device__ __forceinline__ uint64_t lds_u64(uint32_t a) {
   asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void lds_2u64(uint32_t a, uint64_t& x, uint64_t& y) {
-  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+// Fragments of 16 lanes: of each 8 columns (256 bits) a thread has two of row
+// lane / 4 and two of row lane / 4 + 8; of each 128 bits one word of either.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr));
 }
-// Barrier of the 64 threads of warps w and w ^ 4 (ids 1 .. 4).
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id + 1) : "memory"); }
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+               : "memory");
+}
 
 template <int D, bool INT8>
 __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const uint8_t* __restrict__ k_codes,
@@ -140,13 +168,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
   __shared__ TileDesc descs[kTileStages];
   // full: the operand tile is decoded / the scores, weights, queries are in
   // TMEM; free: its reader is done (s_full also frees K's buffer, o_done the
-  // weights').  No barrier can complete two phases past one of its waiters:
-  // each next phase needs what that waiter does after the wait.
-  __shared__ __align__(8) uint64_t k_full[2], v_full[2], v_free[2], s_full[2], s_free[2], w_full, o_done, q_full, idle,
+  // weights').  A wait names a phase by its parity, so its waiter must be
+  // sure of the phase before (it has waited for it, or for something that
+  // followed it), and the phase after must need what it does after the wait.
+  __shared__ __align__(8) uint64_t k_full[2], v_full[2], v_free[2], s_full[2], w_full[2], o_done, o_free, q_full, idle,
       d_full[kTileStages], d_free[kTileStages];
+  // between the groups, per 32 rows: the reference maximum after a tile, and
+  // a group's sums when the other ends the piece (two turns each)
+  __shared__ __align__(8) uint64_t m_full[2][4], l_full[2][2][4];
+  __shared__ float m_turn[2][kTileRows], l_turn[2][2][kTileRows], lm_turn[2][2][kTileRows];
   __shared__ uint32_t tmem_ptr;
-  __shared__ float swap_a[2][kTileRows], swap_m[2][kTileRows], swap_l[2][kTileRows];  // between partners
-  __shared__ bool pair_ok[2][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
   const uint32_t k_tile = base, v_tile = base + 2 * S::kOperand, scales = base + 4 * S::kOperand;
@@ -154,17 +185,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4);
       mbar_init(&v_full[i], 4);
-      mbar_init(&s_full[i], 1);
       mbar_init(&v_free[i], 1);
-      mbar_init(&s_free[i], 8);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&w_full[i], 4);
+      for (int r = 0; r < 4; ++r) {
+        mbar_init(&m_full[i][r], 1);
+        mbar_init(&l_full[i][0][r], 1);
+        mbar_init(&l_full[i][1][r], 1);
+      }
     }
-    mbar_init(&w_full, 8);
     mbar_init(&o_done, 1);
-    mbar_init(&q_full, 8);
+    mbar_init(&o_free, 4);
+    mbar_init(&q_full, 4);
     mbar_init(&idle, 1);
     for (int i = 0; i < kTileStages; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_free[i], 13);  // softmax, decode and MMA warps
+      mbar_init(&d_free[i], 9);  // 4 softmax and 4 decode warps, the MMA warp
     }
     fence_barrier_init();
   }
@@ -174,225 +210,334 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
   }
   griddep_launch_dependents();
   griddep_wait();
+  tc_fence_before();
   const Share share = plan_units(p, kTileRows, kTilePos, sched);  // also orders the barriers' set-up
   tc_fence_after();
   const uint32_t tmem = tmem_ptr;
   const bool works = (int)blockIdx.x < share.ctas && share.total > 0;
   const int u0 = works ? share.begin(blockIdx.x) : 0, u1 = works ? share.begin(blockIdx.x + 1) : 0;
   const int tiles = u1 - u0;
+  if (threadIdx.x == 480) p.records[blockIdx.x] = merge_record(p, sched, share, kTileRows);
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = mbar_wait(bar, parity, p.err, p.wait_ns);
+    if (ok && !mbar_test_wait(bar, parity)) ok = tile_spin(bar, parity, p.err, p.wait_ns);
     return ok;
   };
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax --
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    constexpr int OC = D / 2;     // accumulator columns of this thread
-    float m = kNegInf, power = 0.f;
-    uint64_t l2 = 0;
-    int tok = -1;
-    bool live_warp = false;
-    int st = 0;
-    uint32_t ring = 0;  // parity of the descriptors' turn
-    // Partners agree on whether the next descriptor is there: what it says
-    // decides which of the pair's barriers they meet at.  (The barrier also
-    // ends the turn's use of swap_m.)
-    auto open = [&]() {
-      wait(&d_full[st], ring);
-      __syncwarp();
-      if (lane == 0) pair_ok[half][warp & 3] = ok;
-      pair_sync(warp & 3);
-      return pair_ok[0][warp & 3] && pair_ok[1][warp & 3];
-    };
-    bool have = tiles > 0 && open();
+    // Row i of a thread (i < 4) is row rw + 8 i + lane / 4; its positions are
+    // 8 k + 2 (lane % 4) and the next, k < 16.
+    const int group = warp >> 2, quarter = warp & 3, rw = quarter * 32, g = lane >> 2, t = lane & 3;
+    const uint32_t lanes = tmem + ((uint32_t)rw << 16);
+    float m[4], power[4];
+    uint64_t l2[4];
+    int tok[4];
+    int item = -1, made = 0, taken = 0;
+    bool live = false;
 #pragma unroll 1
-    for (int j = 0; j < tiles && have; ++j) {
+    for (int j = group; j < tiles; j += 2) {
+      const int st = j % kTileStages;
+      wait(&d_full[st], (j / kTileStages) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
       const TileDesc& x = descs[st];
-      const bool first = x.first, last = x.last;
-      if (first) {
-        // queries: f16, the row's largest magnitude brought to [2^14, 2^15);
-        // this thread's half of the channels
-        const int r = x.row0 + row;
-        live_warp = x.row0 + (warp & 3) * 32 < x.rows;
-        tok = r < x.rows ? r / p.group : -1;
-        const __nv_bfloat16* src =
-            tok < 0 ? nullptr
-                    : p.q + (size_t)(x.tok0 + tok) * p.ldq + (x.head * p.group + r - tok * p.group) * D + half * (D / 2);
-        uint32_t q[D / 4];
+      if (x.item != item) {
+        // a new piece: its queries, f16, each row's largest magnitude brought
+        // to [2^14, 2^15).  The group of its first tile stores them; the
+        // other needs the powers alone.  Row rw + lane here.
+        item = x.item;
+        live = x.row0 + rw < x.rows;
+        const int r = x.row0 + rw + lane;
+        const int mine = r < x.rows ? r / p.group : -1;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (size_t)(x.tok0 + max(mine, 0)) * p.ldq + (x.head * p.group + (mine < 0 ? 0 : r - mine * p.group)) * D);
         float amax = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = mine >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 v = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
-          q[4 * c] = v.x;
-          q[4 * c + 1] = v.y;
-          q[4 * c + 2] = v.z;
-          q[4 * c + 3] = v.w;
+          for (int e = 0; e < 4; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
         }
-#pragma unroll
-        for (int c = 0; c < D / 4; ++c)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(q[c] << 16)), fabsf(__uint_as_float(q[c] & 0xffff0000u))));
-        swap_a[half][row] = amax;
-        pair_sync(warp & 3);
-        amax = fmaxf(amax, swap_a[half ^ 1][row]);
         float up, down;
         row_power(amax, up, down);
-        power = down * p.scale_log2;
+        if (x.first) {
+          // the last piece's scores are done with the columns
+          if (j > 0) wait(&s_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
+          if (__all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+              uint32_t f[16];
 #pragma unroll
-        for (int c = 0; c < D / 4; ++c) {
-          const __half2 h =
-              __floats2half2_rn(__uint_as_float(q[c] << 16) * up, __uint_as_float(q[c] & 0xffff0000u) * up);
-          q[c] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        tmem_st(lanes + kTmemQ + half * (D / 4), q);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
-        m = kNegInf;
-        l2 = 0;
-      }
-      const uint32_t sc = scales + st * S::kScales + half * 64 * 4;
-      wait(&s_full[j & 1], (j >> 1) & 1);
-      float t[64];
-      float top = kNegInf;
-      if (live_warp && __all_sync(0xffffffffu, ok)) {
-        tc_fence_after();
-        uint32_t lo[32], hi[32];
-        tmem_ld32(lanes + kTmemS + (j & 1) * 128 + half * 64, lo);
-        tmem_ld32(lanes + kTmemS + (j & 1) * 128 + half * 64 + 32, hi);
-        tmem_ld_wait();
+              for (int c = 0; c < 4; ++c) {
+                const uint4 v = mine >= 0 ? __ldg(src + 4 * h + c) : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          t[i] = __uint_as_float(lo[i]);
-          t[i + 32] = __uint_as_float(hi[i]);
-        }
-        const uint64_t pw = pack_f32x2(power, power);
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          uint64_t ka, kb, va, vb;
-          lds_2u64(sc + i * 4, ka, kb);
-          lds_2u64(sc + kTilePos * 4 + i * 4, va, vb);
-          unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(t[i], t[i + 1]), pw), ka, va), t[i], t[i + 1]);
-          unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(t[i + 2], t[i + 3]), pw), kb, vb), t[i + 2], t[i + 3]);
-        }
-        if (x.before < kTilePos || x.count < kTilePos) {
-          const unsigned long long see = seen_bits(p, x.tok0, tok, x.count - half * 64, x.before - half * 64);
-          const uint32_t see_lo = (uint32_t)see, see_hi = (uint32_t)(see >> 32);
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!((i < 32 ? see_lo >> i : see_hi >> (i - 32)) & 1)) t[i] = kNegInf;
-        }
-#pragma unroll
-        for (int i = 0; i < 64; ++i) top = fmaxf(top, t[i]);
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[j & 1]);
-      swap_m[half][row] = top;
-      pair_sync(warp & 3);
-      top = fmaxf(top, swap_m[half ^ 1][row]);
-      const bool grown = top > m + kRescaleAt || (m == kNegInf && top > kNegInf);
-      // the accumulator, the weights' columns and (below) the sums follow the
-      // previous tile's product
-      if (j > 0) wait(&o_done, (j - 1) & 1);
-      if (live_warp && __all_sync(0xffffffffu, ok)) {
-        tc_fence_after();
-        if (__any_sync(0xffffffffu, grown)) {
-          const float f = grown ? ex2(m - top) : 1.f;
-          if (grown) m = top;
-          l2 = mul_f32x2(l2, pack_f32x2(f, f));
-          if (!first) {
-#pragma unroll
-            for (int c = 0; c < OC; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(lanes + kTmemO + half * OC + c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st(lanes + kTmemO + half * OC + c, o);
-            }
-          }
-        }
-        const float ref = m == kNegInf ? 0.f : -m;
-        uint32_t wt[32];
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          uint64_t ia, ib;
-          lds_2u64(sc + 2 * kTilePos * 4 + i * 4, ia, ib);
-          const float a = ex2(t[i] + ref), b = ex2(t[i + 1] + ref), c = ex2(t[i + 2] + ref), d = ex2(t[i + 3] + ref);
-          l2 = fma_f32x2(pack_f32x2(a, b), ia, l2);
-          l2 = fma_f32x2(pack_f32x2(c, d), ib, l2);
-          const __half2 h0 = __floats2half2_rn(a, b), h1 = __floats2half2_rn(c, d);
-          wt[i / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-          wt[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-        }
-        tmem_st(lanes + kTmemW + half * 32, wt);
-        tmem_st_wait();
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&w_full);
-
-      if (last) {
-        // the item's (or this part's) result
-        float la, lb;
-        unpack_f32x2(l2, la, lb);
-        float l = la + lb;
-        swap_l[half][row] = l;
-        pair_sync(warp & 3);
-        l += swap_l[half ^ 1][row];
-        if (l != l) m = 0.f;  // a NaN row keeps its place in the merge
-        wait(&o_done, j & 1);
-        if (live_warp && __all_sync(0xffffffffu, ok)) {
-          tc_fence_after();
-          const bool whole = x.whole, write = tok >= 0;
-          const int r = x.row0 + row;
-          float* part = p.partial + (size_t)x.slot * kTileRows * (D + 2);
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const size_t tk = write ? x.tok0 + tok : 0;
-          const int h = write ? x.head * p.group + r - tok * p.group : 0;
-#pragma unroll
-          for (int c = 0; c < OC; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(lanes + kTmemO + half * OC + c, o);
-            tmem_ld_wait();
-            if (write && whole) {
-              __nv_bfloat16* dst = p.out + tk * p.ldo + h * D + half * OC + c;
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                // a row that saw nothing: zeros (its weights were all zero)
-                __nv_bfloat162 v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  v[e] = __floats2bfloat162_rn(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
-                reinterpret_cast<uint4*>(dst + i)[0] = *reinterpret_cast<const uint4*>(v);
+                for (int e = 0; e < 4; ++e) {
+                  const __half2 y =
+                      __floats2half2_rn(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+                  f[4 * c + e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
               }
-            } else if (write) {
-              float* dst = part + row * D + half * OC + c;
+              tmem_st(lanes + kTmemQ + h * 16, f);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full);
+        }
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        for (int i = 0; i < 4; ++i) {
+          power[i] = __shfl_sync(0xffffffffu, down, 8 * i + g) * p.scale_log2;
+          tok[i] = __shfl_sync(0xffffffffu, mine, 8 * i + g);
+          m[i] = kNegInf;
+          l2[i] = 0;
+        }
+      }
+      const uint32_t sc = scales + st * S::kScales + t * 8;
+      const uint32_t s_at = lanes + kTmemS + (j & 1) * 128;
+      wait(&s_full[j & 1], (j >> 1) & 1);
+      const bool run = live && __all_sync(0xffffffffu, ok);
+      // Two passes over the tile's two halves of 64 positions: the maximum,
+      // then the weights.  Scores are formed again from TMEM rather than held
+      // (128 registers of them left the code spilled and twice as long).
+      // sv[h]: rows 2 h and 2 h + 1 of the thread.
+      const bool part_seen = x.before < kTilePos || x.count < kTilePos;
+      float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, ref[4];
+      if (run) tc_fence_after();
+#pragma unroll 1
+      for (int pass = 0; pass < 4; ++pass) {
+        const int c = pass & 1;
+        if (pass == 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+          }
+          // the reference the other group left, and the one from here on
+          if (j > 0) wait(&m_full[(j - 1) & 1][quarter], ((j - 1) >> 1) & 1);
+          float f[4];          // the accumulator's factor
+          bool grown = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float old = x.first ? kNegInf : m_turn[(j - 1) & 1][rw + 8 * i + g];
+            const bool up = top[i] > old + kRescaleAt || (old == kNegInf && top[i] > kNegInf);
+            const float now = up ? top[i] : old;
+            f[i] = up ? ex2(old - now) : 1.f;
+            grown |= up;
+            if (now != m[i]) {
+              const float c = ex2(m[i] - now);  // m = -inf: 0
+              l2[i] = mul_f32x2(l2[i], pack_f32x2(c, c));
+              m[i] = now;
             }
           }
-          if (write && half == 0) {
-            if (whole) {
-              if (p.lse != nullptr)
-                p.lse[tk * p.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
-            } else {
-              part[kTileRows * D + row] = m;
-              part[kTileRows * D + kTileRows + row] = l;
+          if (t == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m_turn[j & 1][rw + 8 * i + g] = m[i];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m_full[j & 1][quarter]);
+          if (run && !x.first && __any_sync(0xffffffffu, grown)) {
+            wait(&o_done, (j - 1) & 1);
+            if (__all_sync(0xffffffffu, ok)) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t o[16];
+                  tmem_ld_16x256b(lanes + ((uint32_t)(16 * h) << 16) + kTmemO + c, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) * ((e & 2) ? f[2 * h + 1] : f[2 * h]));
+                  tmem_st_16x256b(lanes + ((uint32_t)(16 * h) << 16) + kTmemO + c, o);
+                }
             }
           }
-          tc_fence_before();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ref[i] = m[i] == kNegInf ? 0.f : -m[i];
+        }
+        if (!run) continue;
+        __syncwarp();
+        uint32_t sv[2][32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld_16x256b(s_at + ((uint32_t)(16 * h) << 16) + 64 * c, sv[h]);
+        tmem_ld_wait();
+        const uint32_t at = sc + c * 256;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t ks = lds_u64(at + k * 32), vs = lds_u64(at + kTilePos * 4 + k * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t& a = sv[i >> 1][4 * k + (i & 1) * 2];
+            uint32_t& b = sv[i >> 1][4 * k + (i & 1) * 2 + 1];
+            const uint64_t raw = pack_f32x2(__uint_as_float(a), __uint_as_float(b));
+            unpack_u32x2(fma_f32x2(mul_f32x2(raw, pack_f32x2(power[i], power[i])), ks, vs), a, b);
+          }
+        }
+        if (part_seen) {
+          uint32_t bits[4][2];
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int tk = i == 0 ? tok[0] : i == 1 ? tok[1] : i == 2 ? tok[2] : tok[3];
+            const unsigned long long see =
+                seen_bits(p, x.tok0, tk, x.count - c * 64, x.before - c * 64) >> (2 * t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e == i) {
+                bits[e][0] = (uint32_t)see;
+                bits[e][1] = (uint32_t)(see >> 32);
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!((bits[i][k >> 2] >> ((k & 3) * 8 + e)) & 1))
+                  sv[i >> 1][4 * k + (i & 1) * 2 + e] = __float_as_uint(kNegInf);
+          __syncwarp();
+        }
+        if (pass < 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              top[i] = fmaxf(top[i], fmaxf(__uint_as_float(sv[i >> 1][4 * k + (i & 1) * 2]),
+                                           __uint_as_float(sv[i >> 1][4 * k + (i & 1) * 2 + 1])));
+          continue;
+        }
+        // the weights go over the scores, 32 columns for 64: what they cover is read
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t iv = lds_u64(at + 2 * kTilePos * 4 + k * 32);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int i = 2 * h + e;
+              float u, v;
+              unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(sv[h][4 * k + 2 * e]),
+                                                __uint_as_float(sv[h][4 * k + 2 * e + 1])),
+                                     pack_f32x2(ref[i], ref[i])),
+                           u, v);
+              u = ex2(u);
+              v = ex2(v);
+              l2[i] = fma_f32x2(pack_f32x2(u, v), iv, l2[i]);
+              const __half2 y = __floats2half2_rn(u, v);
+              w[2 * k + e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
+          tmem_st_16x128b(s_at + ((uint32_t)(16 * h) << 16) + 32 * c, w);
+        }
+      }
+      if (run) {
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      // the wait for this product, below, has to know that the one before is
+      // over; it is sure of that only while this one cannot have begun
+      if (x.last && j > 0) wait(&o_done, (j - 1) & 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_full[j & 1]);
+
+      if (x.last || x.next_last) {
+        float l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a, b;
+          unpack_f32x2(l2[i], a, b);
+          a += b;
+          a += __shfl_xor_sync(0xffffffffu, a, 1);
+          a += __shfl_xor_sync(0xffffffffu, a, 2);
+          l[i] = a;
+        }
+        if (x.next_last) {
+          // the other group ends the piece
+          const int turn = made & 1;
+          if (t == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              l_turn[group][turn][rw + 8 * i + g] = l[i];
+              lm_turn[group][turn][rw + 8 * i + g] = m[i];
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&l_full[group][turn][quarter]);
+          ++made;
+        } else {
+          if (!x.first) {
+            const int turn = taken & 1;
+            wait(&l_full[group ^ 1][turn][quarter], (taken >> 1) & 1);
+            ++taken;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float other = lm_turn[group ^ 1][turn][rw + 8 * i + g];
+              if (other != kNegInf) l[i] = fmaf(l_turn[group ^ 1][turn][rw + 8 * i + g], ex2(other - m[i]), l[i]);
+              else l[i] += l_turn[group ^ 1][turn][rw + 8 * i + g];  // zero, or NaN
+            }
+          }
+          wait(&o_done, j & 1);
+          if (live && __all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+            const bool whole = x.whole;
+            float* part = p.partial + (size_t)x.slot * kTileRows * (D + 2);
+            float inv[4];
+            size_t at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (l[i] != l[i]) m[i] = 0.f;  // a NaN row keeps its place in the merge
+              // a row that saw nothing: zeros (its weights were all zero)
+              inv[i] = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
+              const int row = rw + 8 * i + g, r = x.row0 + row;
+              const size_t tk = x.tok0 + max(tok[i], 0);
+              const int h = tok[i] < 0 ? 0 : x.head * p.group + r - tok[i] * p.group;
+              at[i] = whole ? tk * p.ldo + h * D + 2 * t : (size_t)row * D + 2 * t;
+              if (t == 0 && tok[i] >= 0) {
+                if (!whole) {
+                  part[kTileRows * D + row] = m[i];
+                  part[kTileRows * D + kTileRows + row] = l[i];
+                } else if (p.lse != nullptr) {
+                  p.lse[tk * p.q_heads + h] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+                }
+              }
+            }
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t o[16];
+                tmem_ld_16x256b(lanes + ((uint32_t)(16 * h) << 16) + kTmemO + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int r = 2 * h + i;
+                  if (tok[r] < 0) continue;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const float a = __uint_as_float(o[4 * k + 2 * i]) * inv[r];
+                    const float b = __uint_as_float(o[4 * k + 2 * i + 1]) * inv[r];
+                    if (whole)
+                      *reinterpret_cast<__nv_bfloat162*>(p.out + at[r] + c + 8 * k) = __floats2bfloat162_rn(a, b);
+                    else
+                      *reinterpret_cast<float2*>(part + at[r] + c + 8 * k) = make_float2(a, b);
+                  }
+                }
+              }
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_free);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&d_free[st]);
-      if (++st == kTileStages) st = 0, ring ^= 1;
-      if (j + 1 < tiles) have = open();
     }
   } else if (warp < 12) {
     // -------------------------------------------------------------- decode --
@@ -422,18 +567,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
         if (lane == 0) mbar_arrive(&d_free[st]);
       }
     };
+    // chunk (c % 4) * 2 + e of row r sits at that ^ (r % 8); rows RPI apart
+    // differ by RPI * 128 bytes and, for RPI = 4, in bit 2 of r % 8
+    const uint32_t line = (D == 128 ? (uint32_t)(c >> 2) * (kTilePos * 128) : 0u) + r0 * 128;
+    const uint32_t chunk0 = (((c & 3) * 2) ^ (r0 & 7)) << 4, chunk1 = (((c & 3) * 2 + 1) ^ (r0 & 7)) << 4;
     auto store = [&](uint32_t tile, const uint4 (&buf)[N]) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int r = r0 + i * RPI;
-        const uint32_t line = tile + (D == 128 ? (uint32_t)(c >> 2) * (kTilePos * 128) : 0u) + r * 128;
+        const uint32_t flip = D == 128 && (i & 1) ? 64u : 0u;
         const uint32_t w[4] = {buf[i].x, buf[i].y, buf[i].z, buf[i].w};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t f[4];
           decode4<INT8>(w[2 * e], f[0], f[1]);
           decode4<INT8>(w[2 * e + 1], f[2], f[3]);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((((c & 3) * 2 + e) ^ (r & 7)) << 4)),
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + line + ((e ? chunk1 : chunk0) ^ flip) +
+                                                                        i * RPI * 128),
                        "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
                        : "memory");
         }
@@ -462,52 +611,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       }
       if (i < tiles) load(i, v_codes, vb, true);
     }
-  } else if (warp == 12) {
+  } else {
+    if (warp == 12) {
     // ----------------------------------------------------------------- MMA --
     if (lane == 0) {
       const uint64_t kd = sdesc_sw128(k_tile), vd = sdesc_mn_sw128(v_tile, kTilePos * 128);
-      int queries = 0;
-      bool first = false;  // tile j + 1 is the first of its piece
-      auto look = [&](int j) {
-        const int st = j % kTileStages;
-        if (!wait(&d_full[st], (j / kTileStages) & 1)) return;
-        first = descs[st].first;
-        mbar_arrive(&d_free[st]);
-      };
-      auto scores = [&](int j) {
-        if (first && !wait(&q_full, queries++ & 1)) return;
-        if (!wait(&k_full[j & 1], (j >> 1) & 1)) return;
-        if (j >= 2 && !wait(&s_free[j & 1], ((j - 2) >> 1) & 1)) return;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_f16_ts(tmem + kTmemS + (j & 1) * 128, tmem + kTmemQ + 8 * k,
-                     kd + (((j & 1) * S::kOperand + (k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4),
-                     idesc_f16(kTilePos, false), k > 0);
-        mma_commit(&s_full[j & 1]);
-      };
-      // turn j: scores of tile j + 1, then the product of tile j; the other
-      // way round where a piece starts: its first scores need its queries,
-      // which wait for the last piece's last product
+      int pieces = 0;       // started with their scores
+      bool first = false;   // tile j + 1 opens its piece
+      // turn j: scores of tile j + 1, then the product of tile j
 #pragma unroll 1
       for (int j = -1; j < tiles && ok; ++j) {
-        const bool start = j >= 0 && first;  // tile j opens its piece
-        if (j + 1 < tiles) look(j + 1);
-        else first = false;
-#pragma unroll 1
-        for (int part = 0; part < 2 && ok; ++part) {
-          if ((part == 1) == first) {
-            if (j + 1 < tiles) scores(j + 1);
-          } else if (j >= 0) {
-            if (!wait(&w_full, j & 1) || !wait(&v_full[j & 1], (j >> 1) & 1)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kTilePos / 16; ++k)
-              mma_f16_ts(tmem + kTmemO, tmem + kTmemW + 8 * k, vd + (((j & 1) * S::kOperand + k * 2048) >> 4),
-                         idesc_f16(D, true), !start || k > 0);
-            mma_commit(&o_done);
-            mma_commit(&v_free[j & 1]);
-          }
+        const bool opens = j >= 0 && first;  // tile j opens its piece
+        const int before = pieces - 1;       // pieces before tile j's, if it opens one
+        if (j + 1 < tiles) {
+          const int n = j + 1, st = n % kTileStages;
+          if (!wait(&d_full[st], (n / kTileStages) & 1)) break;
+          first = descs[st].first;
+          mbar_arrive(&d_free[st]);
+          if (first && !wait(&q_full, pieces++ & 1)) break;
+          if (!wait(&k_full[n & 1], (n >> 1) & 1)) break;
+          if (n >= 2 && !wait(&o_done, (n - 2) & 1)) break;  // the weights in these columns
+          tc_fence_after();
+#pragma unroll 2
+          for (int k = 0; k < D / 16; ++k)
+            mma_f16_ts(tmem + kTmemS + (n & 1) * 128, tmem + kTmemQ + 8 * k,
+                       kd + (((n & 1) * S::kOperand + (k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4),
+                       idesc_f16(kTilePos, false), k > 0);
+          mma_commit(&s_full[n & 1]);
+        }
+        if (j >= 0) {
+          if (!wait(&w_full[j & 1], (j >> 1) & 1) || !wait(&v_full[j & 1], (j >> 1) & 1)) break;
+          if (opens && before > 0 && !wait(&o_free, (before - 1) & 1)) break;
+          tc_fence_after();
+#pragma unroll 2
+          for (int k = 0; k < kTilePos / 16; ++k)
+            mma_f16_ts(tmem + kTmemO, tmem + kTmemS + (j & 1) * 128 + 8 * k,
+                       vd + (((j & 1) * S::kOperand + k * 2048) >> 4), idesc_f16(D, true), !opens || k > 0);
+          mma_commit(&o_done);
+          mma_commit(&v_free[j & 1]);
         }
       }
       // MMAs still in flight (a wait ran out) end before TMEM is given up
@@ -515,28 +656,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       (void)mbar_wait(&idle, 0, p.err, p.wait_ns);
     }
     __syncwarp();
-  } else if (warp == 13) {
-    // ------------------------------------------------- scales and prefetch --
-    // A turn loads what tile j + 1 needs before it hands over tile j.  Lane i
-    // has positions 4 i .. 4 i + 3: within one run of 16, whose row its first
-    // lane hands on.
+    } else {
+    // ----------------------------------------------------- the tiles ahead --
+    // Warp 13 + i takes tiles i, i + 3, ...: the chain from page table to
+    // scales is longer than a tile's turn.  Lane i has positions 4 i .. 4 i + 3:
+    // within one run of 16, whose row its first lane hands on.
     Piece x = {};
-    int tile = 0, len = 0;
-    auto step = [&](int j) {
-      if (j == 0 || tile + 1 == x.unit1) {
-        x = find_piece(p, sched, kTileRows, u0 + j, u1);
-        tile = x.unit0;
-        len = sched.len[x.seq];
-      } else {
-        ++tile;
+    int item = 0, done = 0;  // units of the item at hand: [item, done)
+#pragma unroll 1
+    for (int j = warp - 13; j < tiles; j += 3) {
+      const int u = u0 + j;
+      if (u >= done) {
+        x = find_piece(p, sched, kTileRows, u, u1);
+        item = u - x.unit0;
+        done = item + x.units;
       }
-    };
-    int row = 0, count = 0;
-    float4 ks = {}, vs = {};
-    auto fetch = [&]() {
-      count = len - tile * kTilePos;
-      row = 0;
-      ks = vs = make_float4(1.f, 1.f, 1.f, 1.f);
+      const int tile = u - item, count = sched.len[x.seq] - tile * kTilePos;
+      int row = 0;
+      float4 ks = make_float4(1.f, 1.f, 1.f, 1.f), vs = ks;
       if (lane * 4 < count) {
         const int pos = tile * kTilePos + lane * 4;
         const int page = min(max(__ldg(p.table + (size_t)x.seq * p.ldp + (pos >> p.page_shift)), 0), p.pages - 1);
@@ -548,30 +685,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
           bulk_prefetch_l2(v_codes + (size_t)row * D, 16 * D);
         }
       }
-    };
-    if (tiles > 0) {
-      step(0);
-      fetch();
-    }
-    int st = 0;
-    uint32_t ring = 1;
-#pragma unroll 1
-    for (int j = 0; j < tiles; ++j) {
-      if (j >= kTileStages) wait(&d_free[st], ring);
+      const int st = j % kTileStages;
+      if (j >= kTileStages) wait(&d_free[st], (j / kTileStages - 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       TileDesc& d = descs[st];
       if ((lane & 3) == 0) d.run[lane >> 2] = row;
       if (lane == 0) {
         d.count = count;
         d.before = count - sched.n[x.seq];
-        d.first = j == 0 || tile == x.unit0;
-        d.last = tile + 1 == x.unit1;
-        d.whole = x.unit0 == 0 && x.unit1 == x.units;
+        d.item = item;
+        d.first = u == u0 || u == item;
+        d.last = u + 1 == u1 || u + 1 == done;
+        d.next_last = !d.last && (u + 2 == u1 || u + 2 == done);
+        d.whole = item >= u0 && done <= u1;
         d.row0 = x.row0;
         d.rows = min(sched.n[x.seq], p.max_q) * p.group;
         d.tok0 = sched.tok0[x.seq];
         d.head = x.head;
-        d.slot = 2 * blockIdx.x + (j == tile - x.unit0 ? 0 : 1);  // the share's first piece or a later one
+        d.slot = 2 * blockIdx.x + (item <= u0 ? 0 : 1);  // the share's first piece or a later one
       }
       const uint32_t at = scales + st * S::kScales + lane * 16;
       const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {vs.x, vs.y, vs.z, vs.w};
@@ -587,13 +718,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 2 * kTilePos * 4), "f"(b[0]), "f"(b[1]),
                    "f"(b[2]), "f"(b[3])
                    : "memory");
-      if (j + 1 < tiles) {
-        step(j + 1);
-        fetch();
-      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&d_full[st]);
-      if (++st == kTileStages) st = 0, ring ^= 1;
+    }
     }
   }
   tc_fence_before();

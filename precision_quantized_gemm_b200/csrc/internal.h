@@ -97,6 +97,7 @@ struct CacheReadParams {
 cudaError_t launch_cache_read(const CacheReadParams& p, int head_dim, bool int8, cudaStream_t st, bool pdl);
 
 // Kernel parameters of the attention over the cache (attend.cu).
+struct MergeRecord;
 struct AttendParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
@@ -104,7 +105,8 @@ struct AttendParams {
   const int *q_offsets, *kv_len, *table;
   const unsigned long long* mask;  // NULL: causal
   const float *k_scale, *v_scale;
-  float* partial;             // workspace
+  MergeRecord* records; // workspace: one per CTA, then the partial results
+  float* partial;
   int ldq, ldo, ldp, mask_words, q_heads, kv_heads, group, batch, tokens, max_q;
   int pages, page_shift, box_rows;
   float scale_log2;           // softmax scale * log2(e)
@@ -114,7 +116,7 @@ struct AttendParams {
 constexpr int kAttendMaxBatch = 1024;
 size_t attend_workspace(int head_dim, int rows_max, int sms);
 bool attend_tiles(int rows_max);  // whether the tile kernel takes so many rows per key head
-cudaError_t launch_attend(const AttendParams& p, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
+cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
                           const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl);
 
 // GEMM launchers, one per format (each in its own translation unit).
