@@ -5,29 +5,30 @@
 //   S = Q K^T      A = Q (TMEM, f16), B = K (shared, f16, K-major)  -> TMEM fp32
 //   O += W V       A = W (TMEM, f16), B = V (shared, f16, MN-major) -> TMEM fp32
 //
-// 16 warps in four roles, joined by mbarriers:
-//   0-7   softmax: warps 0-3 take the even tiles, 4-7 the odd ones, warp w the
-//         rows 32 (w % 4) .. + 31 (its TMEM lanes).  A thread holds the scores
-//         of 4 rows x 32 positions (the 16x256b fragments: one position's
-//         scales serve 4 rows) and writes the f16 weights over them in TMEM.
-//   8-11  decode: codes from global memory to f16 in the swizzled operand
+// 28 warps in four roles, joined by mbarriers:
+//   0-15  softmax: warps 0-7 take the even tiles, 8-15 the odd ones; each
+//         group has its own scores, accumulator, maxima and sums, which meet
+//         when a piece ends.  A warp has 16 rows (half of the 32 TMEM lanes it
+//         may touch), a thread 2 rows x 32 positions (the 16x256b fragments:
+//         one position's scales serve 8 rows of a load), and writes the f16
+//         weights over the scores in TMEM.
+//   16-23 decode: codes from global memory to f16 in the swizzled operand
 //         tiles, the next tile's codes in registers meanwhile
-//   12    MMA: one thread issues S of tile j + 1 before O of tile j
-//   13-15 the tiles ahead, in turn: where their positions lie, what of them
+//   24    MMA: one thread issues S of tile j + 1 before O of tile j
+//   25-27 the tiles ahead, in turn: where their positions lie, what of them
 //         counts, their scales (log2 and reciprocal once per position), and
 //         the prefetch of their codes into L2
 //
 // What bounds it: per tile the two MMAs are 1024 tensor cycles, the 16384
-// exponentials 1024 cycles of the 16-wide unit, and shared memory carries the
-// decoded tiles twice (64 KB written, 64 KB read by the MMAs: 1024 cycles).
-// That is why Q and W sit in TMEM (from shared memory they would add 64 KB a
-// tile), codes do not pass through shared memory on their way to f16, and the
-// scores are read in the fragment layout: with a row per thread every warp
-// would load every position's three scales for 32 lanes (192 KB a tile).
-// One tile's chain (load, scores, maximum, exponentials, store) is several
-// times that long, so two groups of warps work on two tiles at once; only the
-// rows' reference maximum passes from one group to the other.
-// Only warps 13-15 walk sequences, heads and pages; the others read tile
+// exponentials 1024 cycles of the 16-wide unit, and shared memory carries 160
+// KB (the decoded tiles written and read, Q read): 1280 cycles.  A softmax
+// warp issues an instruction every 6 to 8 cycles (dependent arithmetic,
+// MUFU and shared loads), so it takes 16 of them, and two tiles at once, to
+// fill the issue slots: with 8 warps, whether two to a tile or on alternate
+// tiles, a tile took over 6500 cycles.
+// W sits in TMEM over S, and codes do not pass through shared memory on their
+// way to f16, because shared memory has no room for either in time.
+// Only warps 25-27 walk sequences, heads and pages; the others read tile
 // descriptors.  That is for the instruction cache, which the roles' loops
 // share: with a walk inlined into each role the warps waited for instructions
 // five times as long as they issued.
@@ -41,7 +42,7 @@ namespace qg {
 
 constexpr int kTileRows = 128;
 constexpr int kTilePos = 128;       // positions per tile = unit of work
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 896;
 constexpr int kTileStages = 6;     // descriptors and scales ahead
 constexpr float kRescaleAt = 8.f;   // log2
 
@@ -49,32 +50,40 @@ template <int D>
 struct TileSmem {
   static constexpr int kOperand = kTilePos * D * 2;    // f16 tile of K or V
   static constexpr int kScales = 3 * kTilePos * 4;     // key scale, log2 vs, 1 / vs
-  static constexpr int kTotal = 1024 + 4 * kOperand + kTileStages * kScales;
+  static constexpr int kTotal = 1024 + 5 * kOperand + kTileStages * kScales;  // K, V twice, Q
 };
 // The spin of a wait, out of line: the instruction cache holds one copy.
 __device__ __noinline__ bool tile_spin(uint64_t* bar, uint32_t parity, unsigned int* err, unsigned long long limit) {
   return mbar_wait(bar, parity, err, limit);
 }
 
-// What a tile is; written by warps 13-15.
+// What a tile is; written by warps 25-27.
 struct TileDesc {
   int run[kTilePos / 16];  // cache row of the 1st of each 16 positions
   int count;               // positions of the sequence from the tile's first on (may pass 128)
   int before;              // those before the drafted tokens (may be negative)
   int item;                // its item's first unit
-  int first, last, next_last;  // of its piece; the next tile is its last
+  int index;               // of its piece
+  int last, next_last;     // it ends the piece; the next tile does
   int whole;               // the piece is the whole item
   int row0, rows;          // first row, rows of the sequence
   int tok0, head, slot;    // slot: partial result, when not whole
 };
 // TMEM columns
-constexpr int kTmemS = 0;        // two score tiles of 128; their weights over the first 64
-constexpr int kTmemO = 256;      // D
-constexpr int kTmemQ = 384;      // D / 2
+constexpr int kTmemS = 0;        // a score tile of 128 per group; its weights over the first 64
+constexpr int kTmemO = 256;      // 128 (D used) per group
 constexpr int kTmemCols = 512;
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
   return (1u << 4)                            // D = f32; A, B = f16
          | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] . B[smem]
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 // D[tmem] (+)= A[tmem, f16] . B[smem]
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -94,24 +103,6 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t mn_s
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
-}
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
-          r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
@@ -139,23 +130,23 @@ __device__ __forceinline__ uint64_t lds_u64(uint32_t a) {
 }
 // Fragments of 16 lanes: of each 8 columns (256 bits) a thread has two of row
 // lane / 4 and two of row lane / 4 + 8; of each 128 bits one word of either.
-__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-               : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(taddr));
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_16x256b(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-               : "memory");
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-               : "memory");
+__device__ __forceinline__ void tmem_st_16x256b(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x128b(uint32_t taddr, uint32_t (&r)[2]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x1.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, const uint32_t (&r)[2]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%2], {%0,%1};" ::"r"(r[0]), "r"(r[1]), "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr) : "memory");
 }
 
 template <int D, bool INT8>
@@ -166,45 +157,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sched sched;
   __shared__ TileDesc descs[kTileStages];
-  // full: the operand tile is decoded / the scores, weights, queries are in
-  // TMEM; free: its reader is done (s_full also frees K's buffer, o_done the
-  // weights').  A wait names a phase by its parity, so its waiter must be
-  // sure of the phase before (it has waited for it, or for something that
-  // followed it), and the phase after must need what it does after the wait.
-  __shared__ __align__(8) uint64_t k_full[2], v_full[2], v_free[2], s_full[2], w_full[2], o_done, o_free, q_full, idle,
+  // full: the operand tile is decoded / the scores, weights, queries are
+  // there.  s_full also frees K's buffer, o_done V's and the weights'.  A wait
+  // names a phase by its parity, so its waiter must be sure of the phase
+  // before (it has waited for it, or for something that followed it), and the
+  // phase after must need what it does after the wait.
+  __shared__ __align__(8) uint64_t k_full[2], v_full[2], s_full[2], w_full[2], o_done[2], o_free, q_full, idle,
       d_full[kTileStages], d_free[kTileStages];
-  // between the groups, per 32 rows: the reference maximum after a tile, and
-  // a group's sums when the other ends the piece (two turns each)
-  __shared__ __align__(8) uint64_t m_full[2][4], l_full[2][2][4];
-  __shared__ float m_turn[2][kTileRows], l_turn[2][2][kTileRows], lm_turn[2][2][kTileRows];
+  // a group's maxima and sums when the other ends the piece, per warp of 16
+  // rows (two turns each)
+  __shared__ __align__(8) uint64_t l_full[2][2][8];
+  __shared__ float l_turn[2][2][kTileRows], m_turn[2][2][kTileRows];
   __shared__ uint32_t tmem_ptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t k_tile = base, v_tile = base + 2 * S::kOperand, scales = base + 4 * S::kOperand;
+  const uint32_t k_tile = base, v_tile = base + 2 * S::kOperand, q_tile = base + 4 * S::kOperand,
+                 scales = base + 5 * S::kOperand;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 4);
-      mbar_init(&v_full[i], 4);
-      mbar_init(&v_free[i], 1);
+      mbar_init(&k_full[i], 8);
+      mbar_init(&v_full[i], 8);
       mbar_init(&s_full[i], 1);
-      mbar_init(&w_full[i], 4);
-      for (int r = 0; r < 4; ++r) {
-        mbar_init(&m_full[i][r], 1);
+      mbar_init(&w_full[i], 8);
+      mbar_init(&o_done[i], 1);
+      for (int r = 0; r < 8; ++r) {
         mbar_init(&l_full[i][0][r], 1);
         mbar_init(&l_full[i][1][r], 1);
       }
     }
-    mbar_init(&o_done, 1);
-    mbar_init(&o_free, 4);
-    mbar_init(&q_full, 4);
+    mbar_init(&o_free, 8);
+    mbar_init(&q_full, 8);
     mbar_init(&idle, 1);
     for (int i = 0; i < kTileStages; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_free[i], 9);  // 4 softmax and 4 decode warps, the MMA warp
+      mbar_init(&d_free[i], 17);  // 8 softmax and 8 decode warps, the MMA warp
     }
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 24) {
     tmem_alloc(&tmem_ptr, kTmemCols);
     tmem_relinquish();
   }
@@ -217,22 +207,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
   const bool works = (int)blockIdx.x < share.ctas && share.total > 0;
   const int u0 = works ? share.begin(blockIdx.x) : 0, u1 = works ? share.begin(blockIdx.x + 1) : 0;
   const int tiles = u1 - u0;
-  if (threadIdx.x == 480) p.records[blockIdx.x] = merge_record(p, sched, share, kTileRows);
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok && !mbar_test_wait(bar, parity)) ok = tile_spin(bar, parity, p.err, p.wait_ns);
     return ok;
   };
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ------------------------------------------------------------- softmax --
-    // Row i of a thread (i < 4) is row rw + 8 i + lane / 4; its positions are
+    // Row i of a thread (i < 2) is row rw + 8 i + lane / 4; its positions are
     // 8 k + 2 (lane % 4) and the next, k < 16.
-    const int group = warp >> 2, quarter = warp & 3, rw = quarter * 32, g = lane >> 2, t = lane & 3;
-    const uint32_t lanes = tmem + ((uint32_t)rw << 16);
-    float m[4], power[4];
-    uint64_t l2[4];
-    int tok[4];
+    const int group = warp >> 3, part16 = warp & 7, rw = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t s_at = tmem + ((uint32_t)rw << 16) + kTmemS + group * 128;
+    const uint32_t o_at = tmem + ((uint32_t)rw << 16) + kTmemO + group * 128;
+    float m[2], power[2];
+    uint64_t l2[2];
+    int tok[2];
     int item = -1, made = 0, taken = 0;
     bool live = false;
 #pragma unroll 1
@@ -241,56 +232,59 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       wait(&d_full[st], (j / kTileStages) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       const TileDesc& x = descs[st];
-      if (x.item != item) {
-        // a new piece: its queries, f16, each row's largest magnitude brought
-        // to [2^14, 2^15).  The group of its first tile stores them; the
-        // other needs the powers alone.  Row rw + lane here.
+      const bool opens = x.item != item;  // this group's first tile of the piece
+      if (opens) {
+        // its queries, f16, each row's largest magnitude brought to
+        // [2^14, 2^15).  The group of the piece's first tile stores them; the
+        // other needs the powers alone.  Here lanes l and l + 16 share row
+        // rw + l, half of the channels each.
         item = x.item;
         live = x.row0 + rw < x.rows;
-        const int r = x.row0 + rw + lane;
+        const int row = rw + (lane & 15), r = x.row0 + row;
         const int mine = r < x.rows ? r / p.group : -1;
         const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (size_t)(x.tok0 + max(mine, 0)) * p.ldq + (x.head * p.group + (mine < 0 ? 0 : r - mine * p.group)) * D);
+            p.q + (size_t)(x.tok0 + max(mine, 0)) * p.ldq + (x.head * p.group + (mine < 0 ? 0 : r - mine * p.group)) * D +
+            (lane >> 4) * (D / 2));
         float amax = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           const uint4 v = mine >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
         }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
         float up, down;
         row_power(amax, up, down);
-        if (x.first) {
-          // the last piece's scores are done with the columns
+        if (x.index == 0) {
+          // the last piece's scores are done with the queries
           if (j > 0) wait(&s_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
           if (__all_sync(0xffffffffu, ok)) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int h = 0; h < D / 32; ++h) {
-              uint32_t f[16];
+            const uint32_t dst = q_tile + row * 128 + (D == 128 ? (uint32_t)(lane >> 4) * (kTileRows * 128) : 0u);
+#pragma unroll 2
+            for (int c = 0; c < D / 16; ++c) {
+              const uint4 v = mine >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              uint32_t f[4];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint4 v = mine >= 0 ? __ldg(src + 4 * h + c) : make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const __half2 y =
-                      __floats2half2_rn(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
-                  f[4 * c + e] = *reinterpret_cast<const uint32_t*>(&y);
-                }
+              for (int e = 0; e < 4; ++e) {
+                const __half2 y =
+                    __floats2half2_rn(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+                f[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
-              tmem_st(lanes + kTmemQ + h * 16, f);
+              const int chunk = D == 128 ? c : (lane >> 4) * (D / 16) + c;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((chunk ^ (row & 7)) << 4)), "r"(f[0]),
+                           "r"(f[1]), "r"(f[2]), "r"(f[3])
+                           : "memory");
             }
-            tmem_st_wait();
-            tc_fence_before();
+            fence_proxy_async_smem();
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_full);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           power[i] = __shfl_sync(0xffffffffu, down, 8 * i + g) * p.scale_log2;
           tok[i] = __shfl_sync(0xffffffffu, mine, 8 * i + g);
           m[i] = kNegInf;
@@ -298,203 +292,176 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
         }
       }
       const uint32_t sc = scales + st * S::kScales + t * 8;
-      const uint32_t s_at = lanes + kTmemS + (j & 1) * 128;
-      wait(&s_full[j & 1], (j >> 1) & 1);
-      const bool run = live && __all_sync(0xffffffffu, ok);
-      // Two passes over the tile's two halves of 64 positions: the maximum,
-      // then the weights.  Scores are formed again from TMEM rather than held
-      // (128 registers of them left the code spilled and twice as long).
-      // sv[h]: rows 2 h and 2 h + 1 of the thread.
-      const bool part_seen = x.before < kTilePos || x.count < kTilePos;
-      float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, ref[4];
-      if (run) tc_fence_after();
+      // the scores of this tile followed this group's last product (the MMA
+      // thread waits for it): the accumulator may be read and scaled
+      wait(&s_full[group], (j >> 1) & 1);
+      if (live && __all_sync(0xffffffffu, ok)) {
+        tc_fence_after();
+        const bool part_seen = x.before < kTilePos || x.count < kTilePos;
+        // 32 positions at a time
 #pragma unroll 1
-      for (int pass = 0; pass < 4; ++pass) {
-        const int c = pass & 1;
-        if (pass == 2) {
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t at = sc + c * 128;
+          uint32_t sv[16];
+          tmem_ld_16x256b(s_at + 32 * c, sv);
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ks = lds_u64(at + k * 32), vs = lds_u64(at + kTilePos * 4 + k * 32);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t& a = sv[4 * k + 2 * i];
+              uint32_t& b = sv[4 * k + 2 * i + 1];
+              const uint64_t raw = pack_f32x2(__uint_as_float(a), __uint_as_float(b));
+              unpack_u32x2(fma_f32x2(mul_f32x2(raw, pack_f32x2(power[i], power[i])), ks, vs), a, b);
+            }
           }
-          // the reference the other group left, and the one from here on
-          if (j > 0) wait(&m_full[(j - 1) & 1][quarter], ((j - 1) >> 1) & 1);
-          float f[4];          // the accumulator's factor
+          if (part_seen) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t bits =
+                  (uint32_t)(seen_bits(p, x.tok0, tok[i], x.count - c * 32, x.before - c * 32) >> (2 * t));
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (!((bits >> (k * 8 + e)) & 1)) sv[4 * k + 2 * i + e] = __float_as_uint(kNegInf);
+            }
+            __syncwarp();
+          }
+          float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              top[i] = fmaxf(top[i],
+                             fmaxf(__uint_as_float(sv[4 * k + 2 * i]), __uint_as_float(sv[4 * k + 2 * i + 1])));
           bool grown = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float old = x.first ? kNegInf : m_turn[(j - 1) & 1][rw + 8 * i + g];
-            const bool up = top[i] > old + kRescaleAt || (old == kNegInf && top[i] > kNegInf);
-            const float now = up ? top[i] : old;
-            f[i] = up ? ex2(old - now) : 1.f;
-            grown |= up;
-            if (now != m[i]) {
-              const float c = ex2(m[i] - now);  // m = -inf: 0
-              l2[i] = mul_f32x2(l2[i], pack_f32x2(c, c));
-              m[i] = now;
+          for (int i = 0; i < 2; ++i) {
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+            grown |= top[i] > m[i] + kRescaleAt || (m[i] == kNegInf && top[i] > kNegInf);
+          }
+          if (__any_sync(0xffffffffu, grown)) {
+            // sums, accumulator and the tile's first weights follow the new reference
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool up = top[i] > m[i] + kRescaleAt || (m[i] == kNegInf && top[i] > kNegInf);
+              f[i] = up ? ex2(m[i] - top[i]) : 1.f;  // m = -inf: 0
+              if (up) m[i] = top[i];
+              l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
             }
-          }
-          if (t == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m_turn[j & 1][rw + 8 * i + g] = m[i];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&m_full[j & 1][quarter]);
-          if (run && !x.first && __any_sync(0xffffffffu, grown)) {
-            wait(&o_done, (j - 1) & 1);
-            if (__all_sync(0xffffffffu, ok)) {
-              tc_fence_after();
+            if (!opens) {
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32)
+              for (int d = 0; d < D; d += 16) {
+                uint32_t o[8];
+                tmem_ld_16x256b(o_at + d, o);
+                tmem_ld_wait();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint32_t o[16];
-                  tmem_ld_16x256b(lanes + ((uint32_t)(16 * h) << 16) + kTmemO + c, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) * ((e & 2) ? f[2 * h + 1] : f[2 * h]));
-                  tmem_st_16x256b(lanes + ((uint32_t)(16 * h) << 16) + kTmemO + c, o);
-                }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ref[i] = m[i] == kNegInf ? 0.f : -m[i];
-        }
-        if (!run) continue;
-        __syncwarp();
-        uint32_t sv[2][32];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_ld_16x256b(s_at + ((uint32_t)(16 * h) << 16) + 64 * c, sv[h]);
-        tmem_ld_wait();
-        const uint32_t at = sc + c * 256;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t ks = lds_u64(at + k * 32), vs = lds_u64(at + kTilePos * 4 + k * 32);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t& a = sv[i >> 1][4 * k + (i & 1) * 2];
-            uint32_t& b = sv[i >> 1][4 * k + (i & 1) * 2 + 1];
-            const uint64_t raw = pack_f32x2(__uint_as_float(a), __uint_as_float(b));
-            unpack_u32x2(fma_f32x2(mul_f32x2(raw, pack_f32x2(power[i], power[i])), ks, vs), a, b);
-          }
-        }
-        if (part_seen) {
-          uint32_t bits[4][2];
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int tk = i == 0 ? tok[0] : i == 1 ? tok[1] : i == 2 ? tok[2] : tok[3];
-            const unsigned long long see =
-                seen_bits(p, x.tok0, tk, x.count - c * 64, x.before - c * 64) >> (2 * t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (e == i) {
-                bits[e][0] = (uint32_t)see;
-                bits[e][1] = (uint32_t)(see >> 32);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ((e & 2) ? f[1] : f[0]));
+                tmem_st_16x256b(o_at + d, o);
               }
+            }
+            if (c > 0) {
+              tmem_st_wait();
+#pragma unroll 1
+              for (int d = 0; d < 16 * c; d += 4) {
+                uint32_t w[2];
+                tmem_ld_16x128b(s_at + d, w);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                  const __half2 y = __floats2half2_rn(v.x * f[i], v.y * f[i]);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                tmem_st_16x128b(s_at + d, w);
+              }
+            }
           }
+          // the weights go over the scores, 16 columns for 32: what they cover is read
+          const float ref[2] = {m[0] == kNegInf ? 0.f : -m[0], m[1] == kNegInf ? 0.f : -m[1]};
+          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (!((bits[i][k >> 2] >> ((k & 3) * 8 + e)) & 1))
-                  sv[i >> 1][4 * k + (i & 1) * 2 + e] = __float_as_uint(kNegInf);
-          __syncwarp();
-        }
-        if (pass < 2) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              top[i] = fmaxf(top[i], fmaxf(__uint_as_float(sv[i >> 1][4 * k + (i & 1) * 2]),
-                                           __uint_as_float(sv[i >> 1][4 * k + (i & 1) * 2 + 1])));
-          continue;
-        }
-        // the weights go over the scores, 32 columns for 64: what they cover is read
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             const uint64_t iv = lds_u64(at + 2 * kTilePos * 4 + k * 32);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = 2 * h + e;
+            for (int i = 0; i < 2; ++i) {
               float u, v;
-              unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(sv[h][4 * k + 2 * e]),
-                                                __uint_as_float(sv[h][4 * k + 2 * e + 1])),
+              unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(sv[4 * k + 2 * i]), __uint_as_float(sv[4 * k + 2 * i + 1])),
                                      pack_f32x2(ref[i], ref[i])),
                            u, v);
               u = ex2(u);
               v = ex2(v);
               l2[i] = fma_f32x2(pack_f32x2(u, v), iv, l2[i]);
               const __half2 y = __floats2half2_rn(u, v);
-              w[2 * k + e] = *reinterpret_cast<const uint32_t*>(&y);
+              w[2 * k + i] = *reinterpret_cast<const uint32_t*>(&y);
             }
           }
-          tmem_st_16x128b(s_at + ((uint32_t)(16 * h) << 16) + 32 * c, w);
+          tmem_st_16x128b(s_at + 16 * c, w);
         }
-      }
-      if (run) {
         tmem_st_wait();
         tc_fence_before();
       }
-      // the wait for this product, below, has to know that the one before is
-      // over; it is sure of that only while this one cannot have begun
-      if (x.last && j > 0) wait(&o_done, (j - 1) & 1);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&w_full[j & 1]);
+      if (lane == 0) mbar_arrive(&w_full[group]);
 
       if (x.last || x.next_last) {
-        float l[4];
+        float l[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           float a, b;
           unpack_f32x2(l2[i], a, b);
           a += b;
           a += __shfl_xor_sync(0xffffffffu, a, 1);
           a += __shfl_xor_sync(0xffffffffu, a, 2);
           l[i] = a;
+          if (a != a) m[i] = 0.f;  // a NaN row keeps its place in the merges
         }
         if (x.next_last) {
           // the other group ends the piece
           const int turn = made & 1;
           if (t == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               l_turn[group][turn][rw + 8 * i + g] = l[i];
-              lm_turn[group][turn][rw + 8 * i + g] = m[i];
+              m_turn[group][turn][rw + 8 * i + g] = m[i];
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&l_full[group][turn][quarter]);
+          if (lane == 0) mbar_arrive(&l_full[group][turn][part16]);
           ++made;
         } else {
-          if (!x.first) {
+          // o = (own + other's) / l, each brought to the larger reference
+          const bool both = x.index > 0;
+          float f[2] = {1.f, 1.f}, of[2] = {0.f, 0.f};
+          if (both) {
             const int turn = taken & 1;
-            wait(&l_full[group ^ 1][turn][quarter], (taken >> 1) & 1);
+            wait(&l_full[group ^ 1][turn][part16], (taken >> 1) & 1);
             ++taken;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float other = lm_turn[group ^ 1][turn][rw + 8 * i + g];
-              if (other != kNegInf) l[i] = fmaf(l_turn[group ^ 1][turn][rw + 8 * i + g], ex2(other - m[i]), l[i]);
-              else l[i] += l_turn[group ^ 1][turn][rw + 8 * i + g];  // zero, or NaN
+            for (int i = 0; i < 2; ++i) {
+              const float om = m_turn[group ^ 1][turn][rw + 8 * i + g], ol = l_turn[group ^ 1][turn][rw + 8 * i + g];
+              const float now = fmaxf(m[i], om);
+              f[i] = m[i] == kNegInf ? 0.f : ex2(m[i] - now);
+              of[i] = om == kNegInf ? 0.f : ex2(om - now);
+              m[i] = now;
+              l[i] = l[i] * f[i] + ol * of[i];
             }
+            // the group's product is the last before o_free: this wait's phase
+            // follows the one its scores followed
+            wait(&o_done[group ^ 1], ((j - 1) >> 1) & 1);
           }
-          wait(&o_done, j & 1);
+          wait(&o_done[group], (j >> 1) & 1);
           if (live && __all_sync(0xffffffffu, ok)) {
             tc_fence_after();
             const bool whole = x.whole;
             float* part = p.partial + (size_t)x.slot * kTileRows * (D + 2);
-            float inv[4];
-            size_t at[4];
+            size_t at[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (l[i] != l[i]) m[i] = 0.f;  // a NaN row keeps its place in the merge
-              // a row that saw nothing: zeros (its weights were all zero)
-              inv[i] = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
+            for (int i = 0; i < 2; ++i) {
               const int row = rw + 8 * i + g, r = x.row0 + row;
               const size_t tk = x.tok0 + max(tok[i], 0);
               const int h = tok[i] < 0 ? 0 : x.head * p.group + r - tok[i] * p.group;
@@ -507,29 +474,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
                   p.lse[tk * p.q_heads + h] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * 0.6931471805599453f;
                 }
               }
+              if (whole) {
+                // a row that saw nothing: zeros (its weights were all zero)
+                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+                f[i] *= inv;
+                of[i] *= inv;
+              }
             }
+            const uint32_t other = tmem + ((uint32_t)rw << 16) + kTmemO + (group ^ 1) * 128;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32)
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[8], q[8];
+              tmem_ld_16x256b(o_at + c, o);
+              if (both) tmem_ld_16x256b(other + c, q);
+              tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t o[16];
-                tmem_ld_16x256b(lanes + ((uint32_t)(16 * h) << 16) + kTmemO + c, o);
-                tmem_ld_wait();
+              for (int i = 0; i < 2; ++i) {
+                if (tok[i] >= 0) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int r = 2 * h + i;
-                  if (tok[r] < 0) continue;
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float a = __uint_as_float(o[4 * k + 2 * i]) * inv[r];
-                    const float b = __uint_as_float(o[4 * k + 2 * i + 1]) * inv[r];
+                  for (int k = 0; k < 2; ++k) {
+                    float a = __uint_as_float(o[4 * k + 2 * i]) * f[i], b = __uint_as_float(o[4 * k + 2 * i + 1]) * f[i];
+                    if (both) {
+                      a = fmaf(__uint_as_float(q[4 * k + 2 * i]), of[i], a);
+                      b = fmaf(__uint_as_float(q[4 * k + 2 * i + 1]), of[i], b);
+                    }
                     if (whole)
-                      *reinterpret_cast<__nv_bfloat162*>(p.out + at[r] + c + 8 * k) = __floats2bfloat162_rn(a, b);
+                      *reinterpret_cast<__nv_bfloat162*>(p.out + at[i] + c + 8 * k) = __floats2bfloat162_rn(a, b);
                     else
-                      *reinterpret_cast<float2*>(part + at[r] + c + 8 * k) = make_float2(a, b);
+                      *reinterpret_cast<float2*>(part + at[i] + c + 8 * k) = make_float2(a, b);
                   }
                 }
               }
+              __syncwarp();
+            }
             tc_fence_before();
           }
           __syncwarp();
@@ -539,28 +516,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       __syncwarp();
       if (lane == 0) mbar_arrive(&d_free[st]);
     }
-  } else if (warp < 12) {
+  } else if (warp < 24) {
     // -------------------------------------------------------------- decode --
-    // K of tile j + 1 before V of tile j.  A lane holds 16 codes of a row: the
-    // 8 lanes of a store phase are 2 rows x 4 of the 16-byte chunks of one
-    // 64-channel block, which the swizzle spreads over all banks.
+    // K of tile j + 1 before V of tile j; a warp has 16 positions.  A lane
+    // holds 16 codes of a row: the 8 lanes of a store phase are 2 rows x 4 of
+    // the 16-byte chunks of one 64-channel block, which the swizzle spreads
+    // over all banks.
     constexpr int RPI = D == 128 ? 4 : 8;     // rows per warp instruction
-    constexpr int N = 32 / RPI;               // instructions per warp and tile
+    constexpr int N = 16 / RPI;               // instructions per warp and tile
     const int c = D == 128 ? (lane & 3) + ((lane >> 4) << 2) : lane & 3;
-    const int r0 = (warp - 8) * 32 + (D == 128 ? (lane >> 2) & 3 : lane >> 2);
+    const int r0 = D == 128 ? (lane >> 2) & 3 : lane >> 2;   // of the warp's positions
+    const int w0 = (warp - 16) * 16;
     auto load = [&](int j, const uint8_t* codes, uint4 (&buf)[N], bool done) {
       const int st = j % kTileStages;
       wait(&d_full[st], (j / kTileStages) & 1);
       if (!__all_sync(0xffffffffu, ok)) return;
-      const TileDesc& x = descs[st];
-      const int run[2] = {x.run[(warp - 8) * 2], x.run[(warp - 8) * 2 + 1]};
-      const int count = x.count - r0;
+      const int count = descs[st].count - w0 - r0;
+      const uint4* src = reinterpret_cast<const uint4*>(codes + (size_t)(descs[st].run[warp - 16] + r0) * D) + c;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         buf[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (i * RPI < count)
-          buf[i] = __ldg(reinterpret_cast<const uint4*>(
-                             codes + (size_t)(run[i / (N / 2)] + (r0 & 15) + i % (N / 2) * RPI) * D) + c);
+        if (i * RPI < count) buf[i] = __ldg(src + i * RPI * (D / 16));
       }
       if (done) {
         __syncwarp();
@@ -569,7 +545,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
     };
     // chunk (c % 4) * 2 + e of row r sits at that ^ (r % 8); rows RPI apart
     // differ by RPI * 128 bytes and, for RPI = 4, in bit 2 of r % 8
-    const uint32_t line = (D == 128 ? (uint32_t)(c >> 2) * (kTilePos * 128) : 0u) + r0 * 128;
+    const uint32_t line = (D == 128 ? (uint32_t)(c >> 2) * (kTilePos * 128) : 0u) + (w0 + r0) * 128;
     const uint32_t chunk0 = (((c & 3) * 2) ^ (r0 & 7)) << 4, chunk1 = (((c & 3) * 2 + 1) ^ (r0 & 7)) << 4;
     auto store = [&](uint32_t tile, const uint4 (&buf)[N]) {
 #pragma unroll
@@ -604,7 +580,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
         if (i + 1 < tiles) load(i + 1, k_codes, kb, false);
       }
       if (j >= 0) {
-        if (j >= 2) wait(&v_free[j & 1], ((j - 2) >> 1) & 1);
+        if (j >= 2) wait(&o_done[j & 1], ((j - 2) >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         store(v_tile + (j & 1) * S::kOperand, vb);
         if (lane == 0) mbar_arrive(&v_full[j & 1]);
@@ -612,120 +588,124 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       if (i < tiles) load(i, v_codes, vb, true);
     }
   } else {
-    if (warp == 12) {
-    // ----------------------------------------------------------------- MMA --
-    if (lane == 0) {
-      const uint64_t kd = sdesc_sw128(k_tile), vd = sdesc_mn_sw128(v_tile, kTilePos * 128);
-      int pieces = 0;       // started with their scores
-      bool first = false;   // tile j + 1 opens its piece
-      // turn j: scores of tile j + 1, then the product of tile j
-#pragma unroll 1
-      for (int j = -1; j < tiles && ok; ++j) {
-        const bool opens = j >= 0 && first;  // tile j opens its piece
-        const int before = pieces - 1;       // pieces before tile j's, if it opens one
-        if (j + 1 < tiles) {
-          const int n = j + 1, st = n % kTileStages;
-          if (!wait(&d_full[st], (n / kTileStages) & 1)) break;
-          first = descs[st].first;
-          mbar_arrive(&d_free[st]);
-          if (first && !wait(&q_full, pieces++ & 1)) break;
-          if (!wait(&k_full[n & 1], (n >> 1) & 1)) break;
-          if (n >= 2 && !wait(&o_done, (n - 2) & 1)) break;  // the weights in these columns
-          tc_fence_after();
-#pragma unroll 2
-          for (int k = 0; k < D / 16; ++k)
-            mma_f16_ts(tmem + kTmemS + (n & 1) * 128, tmem + kTmemQ + 8 * k,
-                       kd + (((n & 1) * S::kOperand + (k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4),
-                       idesc_f16(kTilePos, false), k > 0);
-          mma_commit(&s_full[n & 1]);
-        }
-        if (j >= 0) {
-          if (!wait(&w_full[j & 1], (j >> 1) & 1) || !wait(&v_full[j & 1], (j >> 1) & 1)) break;
-          if (opens && before > 0 && !wait(&o_free, (before - 1) & 1)) break;
-          tc_fence_after();
-#pragma unroll 2
-          for (int k = 0; k < kTilePos / 16; ++k)
-            mma_f16_ts(tmem + kTmemO, tmem + kTmemS + (j & 1) * 128 + 8 * k,
-                       vd + (((j & 1) * S::kOperand + k * 2048) >> 4), idesc_f16(D, true), !opens || k > 0);
-          mma_commit(&o_done);
-          mma_commit(&v_free[j & 1]);
-        }
-      }
-      // MMAs still in flight (a wait ran out) end before TMEM is given up
-      mma_commit(&idle);
-      (void)mbar_wait(&idle, 0, p.err, p.wait_ns);
-    }
-    __syncwarp();
-    } else {
-    // ----------------------------------------------------- the tiles ahead --
-    // Warp 13 + i takes tiles i, i + 3, ...: the chain from page table to
-    // scales is longer than a tile's turn.  Lane i has positions 4 i .. 4 i + 3:
-    // within one run of 16, whose row its first lane hands on.
-    Piece x = {};
-    int item = 0, done = 0;  // units of the item at hand: [item, done)
-#pragma unroll 1
-    for (int j = warp - 13; j < tiles; j += 3) {
-      const int u = u0 + j;
-      if (u >= done) {
-        x = find_piece(p, sched, kTileRows, u, u1);
-        item = u - x.unit0;
-        done = item + x.units;
-      }
-      const int tile = u - item, count = sched.len[x.seq] - tile * kTilePos;
-      int row = 0;
-      float4 ks = make_float4(1.f, 1.f, 1.f, 1.f), vs = ks;
-      if (lane * 4 < count) {
-        const int pos = tile * kTilePos + lane * 4;
-        const int page = min(max(__ldg(p.table + (size_t)x.seq * p.ldp + (pos >> p.page_shift)), 0), p.pages - 1);
-        row = (page * p.kv_heads + x.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-        ks = __ldg(reinterpret_cast<const float4*>(p.k_scale + row));
-        vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + row));
-        if ((lane & 3) == 0) {
-          bulk_prefetch_l2(k_codes + (size_t)row * D, 16 * D);
-          bulk_prefetch_l2(v_codes + (size_t)row * D, 16 * D);
-        }
-      }
-      const int st = j % kTileStages;
-      if (j >= kTileStages) wait(&d_free[st], (j / kTileStages - 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      TileDesc& d = descs[st];
-      if ((lane & 3) == 0) d.run[lane >> 2] = row;
+    if (warp == 24) {
+      // --------------------------------------------------------------- MMA --
       if (lane == 0) {
-        d.count = count;
-        d.before = count - sched.n[x.seq];
-        d.item = item;
-        d.first = u == u0 || u == item;
-        d.last = u + 1 == u1 || u + 1 == done;
-        d.next_last = !d.last && (u + 2 == u1 || u + 2 == done);
-        d.whole = item >= u0 && done <= u1;
-        d.row0 = x.row0;
-        d.rows = min(sched.n[x.seq], p.max_q) * p.group;
-        d.tok0 = sched.tok0[x.seq];
-        d.head = x.head;
-        d.slot = 2 * blockIdx.x + (item <= u0 ? 0 : 1);  // the share's first piece or a later one
+        const uint64_t qd = sdesc_sw128(q_tile), kd = sdesc_sw128(k_tile), vd = sdesc_mn_sw128(v_tile, kTilePos * 128);
+        int pieces = 0;              // whose scores have begun
+        int index = 0, next = 0;     // of tile j and j + 1 in their pieces
+        // turn j: scores of tile j + 1, then the product of tile j
+#pragma unroll 1
+        for (int j = -1; j < tiles && ok; ++j) {
+          index = next;
+          const int before = pieces - 1;  // pieces before tile j's
+          if (j + 1 < tiles) {
+            const int n = j + 1, st = n % kTileStages, s = n & 1;
+            if (!wait(&d_full[st], (n / kTileStages) & 1)) break;
+            next = descs[st].index;
+            mbar_arrive(&d_free[st]);
+            if (next == 0 && !wait(&q_full, pieces++ & 1)) break;
+            if (!wait(&k_full[s], (n >> 1) & 1)) break;
+            if (n >= 2 && !wait(&o_done[s], ((n - 2) >> 1) & 1)) break;  // the weights in these columns
+            tc_fence_after();
+            const uint64_t kt = kd + ((s * S::kOperand) >> 4);
+#pragma unroll 2
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = ((k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4;
+              mma_f16_ss(tmem + kTmemS + s * 128, qd + at, kt + at, idesc_f16(kTilePos, false), k > 0);
+            }
+            mma_commit(&s_full[s]);
+          }
+          if (j >= 0) {
+            const int s = j & 1;
+            if (!wait(&w_full[s], (j >> 1) & 1) || !wait(&v_full[s], (j >> 1) & 1)) break;
+            // a piece's first product of either group: the last piece is out
+            if (index == 0 && before > 0 && !wait(&o_free, (before - 1) & 1)) break;
+            tc_fence_after();
+            const uint64_t vt = vd + ((s * S::kOperand) >> 4);
+#pragma unroll 2
+            for (int k = 0; k < kTilePos / 16; ++k)
+              mma_f16_ts(tmem + kTmemO + s * 128, tmem + kTmemS + s * 128 + 8 * k, vt + ((k * 2048) >> 4),
+                         idesc_f16(D, true), index > 1 || k > 0);
+            mma_commit(&o_done[s]);
+          }
+        }
+        // MMAs still in flight (a wait ran out) end before TMEM is given up
+        mma_commit(&idle);
+        (void)mbar_wait(&idle, 0, p.err, p.wait_ns);
       }
-      const uint32_t at = scales + st * S::kScales + lane * 16;
-      const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {vs.x, vs.y, vs.z, vs.w};
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) value_scale(v4[i], a[i], b[i]);
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(k4[0]), "f"(k4[1]), "f"(k4[2]),
-                   "f"(k4[3])
-                   : "memory");
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + kTilePos * 4), "f"(a[0]), "f"(a[1]),
-                   "f"(a[2]), "f"(a[3])
-                   : "memory");
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 2 * kTilePos * 4), "f"(b[0]), "f"(b[1]),
-                   "f"(b[2]), "f"(b[3])
-                   : "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d_full[st]);
-    }
+    } else {
+      // --------------------------------------------------- the tiles ahead --
+      // Warp 25 + i takes tiles i, i + 3, ...: the chain from page table to
+      // scales is longer than a tile's turn.  Lane i has positions 4 i .. 4 i
+      // + 3: within one run of 16, whose row its first lane hands on.
+      if (warp == 25 && lane == 0) p.records[blockIdx.x] = merge_record(p, sched, share, kTileRows);
+      __syncwarp();
+      Piece x = {};
+      int item = 0, done = 0;  // units of the item at hand: [item, done)
+#pragma unroll 1
+      for (int j = warp - 25; j < tiles; j += 3) {
+        const int u = u0 + j;
+        if (u >= done) {
+          x = find_piece(p, sched, kTileRows, u, u1);
+          item = u - x.unit0;
+          done = item + x.units;
+        }
+        const int tile = u - item, count = sched.len[x.seq] - tile * kTilePos;
+        int row = 0;
+        float4 ks = make_float4(1.f, 1.f, 1.f, 1.f), vs = ks;
+        if (lane * 4 < count) {
+          const int pos = tile * kTilePos + lane * 4;
+          const int page = min(max(__ldg(p.table + (size_t)x.seq * p.ldp + (pos >> p.page_shift)), 0), p.pages - 1);
+          row = (page * p.kv_heads + x.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+          ks = __ldg(reinterpret_cast<const float4*>(p.k_scale + row));
+          vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + row));
+          if ((lane & 3) == 0) {
+            bulk_prefetch_l2(k_codes + (size_t)row * D, 16 * D);
+            bulk_prefetch_l2(v_codes + (size_t)row * D, 16 * D);
+          }
+        }
+        const int st = j % kTileStages;
+        if (j >= kTileStages) wait(&d_free[st], (j / kTileStages - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        TileDesc& d = descs[st];
+        if ((lane & 3) == 0) d.run[lane >> 2] = row;
+        if (lane == 0) {
+          d.count = count;
+          d.before = count - sched.n[x.seq];
+          d.item = item;
+          d.index = u - max(item, u0);
+          d.last = u + 1 == u1 || u + 1 == done;
+          d.next_last = !d.last && (u + 2 == u1 || u + 2 == done);
+          d.whole = item >= u0 && done <= u1;
+          d.row0 = x.row0;
+          d.rows = min(sched.n[x.seq], p.max_q) * p.group;
+          d.tok0 = sched.tok0[x.seq];
+          d.head = x.head;
+          d.slot = 2 * blockIdx.x + (item <= u0 ? 0 : 1);  // the share's first piece or a later one
+        }
+        const uint32_t at = scales + st * S::kScales + lane * 16;
+        const float v4[4] = {vs.x, vs.y, vs.z, vs.w};
+        float a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) value_scale(v4[i], a[i], b[i]);
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(ks.x), "f"(ks.y), "f"(ks.z), "f"(ks.w)
+                     : "memory");
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + kTilePos * 4), "f"(a[0]), "f"(a[1]),
+                     "f"(a[2]), "f"(a[3])
+                     : "memory");
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 2 * kTilePos * 4), "f"(b[0]), "f"(b[1]),
+                     "f"(b[2]), "f"(b[3])
+                     : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_full[st]);
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 24) tmem_dealloc(tmem, kTmemCols);
 }
 
 }  // namespace qg
