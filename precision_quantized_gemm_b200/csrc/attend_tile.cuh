@@ -329,28 +329,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
             }
             __syncwarp();
           }
-          float top[2] = {kNegInf, kNegInf};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              top[i] = fmaxf(top[i],
-                             fmaxf(__uint_as_float(sv[4 * k + 2 * i]), __uint_as_float(sv[4 * k + 2 * i + 1])));
-          bool grown = false;
+          // whether a score passes its row's reference by more than it may:
+          // each lane asks for its own, the row's maximum is formed only then
+          float top[2][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-            grown |= top[i] > m[i] + kRescaleAt || (m[i] == kNegInf && top[i] > kNegInf);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              top[i][e] = fmaxf(__uint_as_float(sv[2 * i + e]), __uint_as_float(sv[4 + 2 * i + e]));
+#pragma unroll
+            for (int k = 2; k < 4; ++k)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) top[i][e] = fmaxf(top[i][e], __uint_as_float(sv[4 * k + 2 * i + e]));
+            top[i][0] = fmaxf(top[i][0], top[i][1]);
           }
+          // m = -inf (nothing seen yet): anything seen passes it
+          const bool grown = top[0][0] > m[0] + kRescaleAt || top[1][0] > m[1] + kRescaleAt;
           if (__any_sync(0xffffffffu, grown)) {
             // sums, accumulator and the tile's first weights follow the new reference
             float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const bool up = top[i] > m[i] + kRescaleAt || (m[i] == kNegInf && top[i] > kNegInf);
-              f[i] = up ? ex2(m[i] - top[i]) : 1.f;  // m = -inf: 0
-              if (up) m[i] = top[i];
+              float now = top[i][0];
+              now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 1));
+              now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 2));
+              const bool up = now > m[i] + kRescaleAt;
+              f[i] = up ? ex2(m[i] - now) : 1.f;  // m = -inf: 0
+              if (up) m[i] = now;
               l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
             }
             if (!opens) {
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
             if (n >= 2 && !wait(&o_done[s], ((n - 2) >> 1) & 1)) break;  // the weights in these columns
             tc_fence_after();
             const uint64_t kt = kd + ((s * S::kOperand) >> 4);
-#pragma unroll 2
+#pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t at = ((k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4;
               mma_f16_ss(tmem + kTmemS + s * 128, qd + at, kt + at, idesc_f16(kTilePos, false), k > 0);
@@ -623,7 +628,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
             if (index == 0 && before > 0 && !wait(&o_free, (before - 1) & 1)) break;
             tc_fence_after();
             const uint64_t vt = vd + ((s * S::kOperand) >> 4);
-#pragma unroll 2
+#pragma unroll
             for (int k = 0; k < kTilePos / 16; ++k)
               mma_f16_ts(tmem + kTmemO + s * 128, tmem + kTmemS + s * 128 + 8 * k, vt + ((k * 2048) >> 4),
                          idesc_f16(D, true), index > 1 || k > 0);
