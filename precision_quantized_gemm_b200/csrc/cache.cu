@@ -89,22 +89,22 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
         }
       }
     }
-    uint32_t a = absmax_bits8(x);
+    Chunk y;
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (int j = 0; j < 4; ++j) y[j] = pack_f32x2(x[2 * j], x[2 * j + 1]);
+    float a = absmax_chunk(y);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) a = absmax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
     if (!live) continue;
     if (is_q) {
-      uint4 out;
-      __nv_bfloat162* o2 = reinterpret_cast<__nv_bfloat162*>(&out);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o2[j] = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-      reinterpret_cast<uint4*>(p.q_out + (size_t)t * p.ldqo + h * D)[lane] = out;
+      reinterpret_cast<uint4*>(p.q_out + (size_t)t * p.ldqo + h * D)[lane] = pack_chunk(y);
     } else if (store) {
       const size_t row = ((size_t)(slot >> p.page_shift) * p.kv_heads + h << p.page_shift) +
                          (slot & ((1 << p.page_shift) - 1));
-      const float s = row_scale<INT8>(a);
+      float s, inv;
+      row_scale<INT8>(a, s, inv);
       if (lane == 0) (is_k ? p.k_scale : p.v_scale)[row] = s;
-      reinterpret_cast<uint2*>((is_k ? p.k_codes : p.v_codes) + row * D)[lane] = row_codes<INT8>(x, s);
+      reinterpret_cast<uint2*>((is_k ? p.k_codes : p.v_codes) + row * D)[lane] = chunk_codes<INT8>(y, s, inv);
     }
   }
 }

@@ -48,59 +48,60 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
   return __reduce_max_sync(0xffffffffu, l < (int)(blockDim.x >> 5) ? red[l] : 0u);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint4 v;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-  return v;
-}
-
 // x <- norm(x) * (w + offset) + b over the row's `nch` chunks.
 template <int CH>
-__device__ __forceinline__ void norm_row(float (&x)[CH][8], int nch, float inv_n, bool layer, float eps,
+__device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, bool layer, float eps,
                                          const uint4* __restrict__ w, const uint4* __restrict__ b, float offset,
                                          float* red) {
   if (layer) {
-    float s = 0.f;
+    uint64_t s = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += x[i][j];
-    const float mean = cta_sum(s, red) * inv_n;
+      for (int j = 0; j < 4; ++j) s = add_f32x2(s, x[i][j]);
+    float a, c;
+    unpack_f32x2(s, a, c);
+    const float mean = cta_sum(a + c, red) * inv_n;
+    const uint64_t m = pack_f32x2(-mean, -mean);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const bool in = threadIdx.x + i * blockDim.x < nch;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = in ? x[i][j] - mean : 0.f;
+      for (int j = 0; j < 4; ++j) x[i][j] = in ? add_f32x2(x[i][j], m) : 0ull;
     }
   }
-  float q = 0.f;
+  uint64_t q = 0;
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q = fmaf(x[i][j], x[i][j], q);
-  const float r = rsqrtf(cta_sum(q, red + 32) * inv_n + eps);
+    for (int j = 0; j < 4; ++j) q = fma_f32x2(x[i][j], x[i][j], q);
+  float a, c;
+  unpack_f32x2(q, a, c);
+  const float r = rsqrtf(cta_sum(a + c, red + 32) * inv_n + eps);
+  const uint64_t r2 = pack_f32x2(r, r), o2 = pack_f32x2(offset, offset);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c < nch) {
-      float wv[8];
-      unpack8(__ldg(w + c), wv);
+    const int at = threadIdx.x + i * blockDim.x;
+    if (at < nch) {
+      Chunk v;
+      unpack_chunk(__ldg(w + at), v);
+      if (offset != 0.f) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = x[i][j] * r * (wv[j] + offset);
+        for (int j = 0; j < 4; ++j) v[j] = add_f32x2(v[j], o2);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = mul_f32x2(mul_f32x2(x[i][j], r2), v[j]);
       if (b != nullptr) {
-        float bv[8];
-        unpack8(__ldg(b + c), bv);
+        unpack_chunk(__ldg(b + at), v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] += bv[j];
+        for (int j = 0; j < 4; ++j) x[i][j] = add_f32x2(x[i][j], v[j]);
       }
     }
   }
 }
 
 template <int CH>
-__global__ void __launch_bounds__(CH >= 8 ? 512 : 1024) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormParams p) {
   __shared__ float red[160];
   griddep_launch_dependents();
   griddep_wait();
@@ -122,31 +123,34 @@ __global__ void __launch_bounds__(CH >= 8 ? 512 : 1024) norm_kernel(const NormPa
   const uint4* xr = p.x ? reinterpret_cast<const uint4*>(p.x + (size_t)m * p.ldx) : nullptr;
   const uint4* gr = p.gate ? reinterpret_cast<const uint4*>(p.gate + (size_t)m * p.ldg) : nullptr;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 rv[CH];
-  float v[CH][8];
+  uint4 rv[CH], xv[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
     rv[i] = rr && c < nch ? rr[c] : zero;
-    unpack8(xr && c < nch ? xr[c] : zero, v[i]);
+    xv[i] = xr && c < nch ? xr[c] : zero;
   }
+  Chunk v[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) unpack_chunk(xv[i], v[i]);
   if (p.post_norm)
     norm_row<CH>(v, nch, p.inv_n, p.post_norm == QG_NORM_LAYER, p.eps, p.post_weight, p.post_bias, p.weight_offset,
                  red);
+  const uint64_t bs = pack_f32x2(p.block_scale, p.block_scale), rs = pack_f32x2(p.residual_scale, p.residual_scale);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
     if (gr != nullptr && c < nch) {
-      float gv[8];
-      unpack8(gr[c], gv);
+      Chunk gv;
+      unpack_chunk(gr[c], gv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= gv[j];
+      for (int j = 0; j < 4; ++j) v[i][j] = mul_f32x2(v[i][j], gv[j]);
     }
-    float r[8];
-    unpack8(rv[i], r);
+    Chunk r;
+    unpack_chunk(rv[i], r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = fmaf(p.residual_scale, r[j], p.block_scale * v[i][j]);
-    if (p.h != nullptr && c < nch) reinterpret_cast<uint4*>(p.h + (size_t)m * p.ldh)[c] = pack8(v[i]);
+    for (int j = 0; j < 4; ++j) v[i][j] = fma_f32x2(rs, r[j], mul_f32x2(bs, v[i][j]));
+    if (p.h != nullptr && c < nch) reinterpret_cast<uint4*>(p.h + (size_t)m * p.ldh)[c] = pack_chunk(v[i]);
   }
   if (!p.pre_norm) return;
   norm_row<CH>(v, nch, p.inv_n, p.pre_norm == QG_NORM_LAYER, p.eps, p.pre_weight, p.pre_bias, p.weight_offset,
@@ -155,23 +159,26 @@ __global__ void __launch_bounds__(CH >= 8 ? 512 : 1024) norm_kernel(const NormPa
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nch) reinterpret_cast<uint4*>(p.y + (size_t)m * p.ldy)[c] = pack8(v[i]);
+      if (c < nch) reinterpret_cast<uint4*>(p.y + (size_t)m * p.ldy)[c] = pack_chunk(v[i]);
     }
   }
   if (p.q == nullptr) return;
   if (p.format == QG_FP8_DYNAMIC || p.format == QG_W8A8_INT8) {
-    uint32_t a = 0;
+    float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) a = max(a, absmax_bits8(v[i]));
-    a = cta_max(a, reinterpret_cast<uint32_t*>(red + 128));
+    for (int i = 0; i < CH; ++i) a = absmax_nan(a, absmax_chunk(v[i]));
+    // magnitudes' bit patterns are ordered like them, NaN last
+    a = __uint_as_float(cta_max(__float_as_uint(a) & 0x7fffffffu, reinterpret_cast<uint32_t*>(red + 128)));
     const bool int8 = p.format == QG_W8A8_INT8;
-    const float s = int8 ? row_scale<true>(a) : row_scale<false>(a);
+    float s, inv;
+    if (int8) row_scale<true>(a, s, inv);
+    else row_scale<false>(a, s, inv);
     if (threadIdx.x == 0) static_cast<float*>(p.scale)[m] = s;
     uint2* q = reinterpret_cast<uint2*>(p.q + (size_t)m * p.N);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nch) q[c] = int8 ? row_codes<true>(v[i], s) : row_codes<false>(v[i], s);
+      if (c < nch) q[c] = int8 ? chunk_codes<true>(v[i], s, inv) : chunk_codes<false>(v[i], s, inv);
     }
   } else if (p.format == QG_BLOCK_FP8) {
     // a 128-element group is 16 chunks, held by 16 neighbouring threads
@@ -180,32 +187,39 @@ __global__ void __launch_bounds__(CH >= 8 ? 512 : 1024) norm_kernel(const NormPa
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      uint32_t a = absmax_bits8(v[i]);
+      float a = absmax_chunk(v[i]);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+      for (int o = 8; o > 0; o >>= 1) a = absmax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
       if (c < nch) {
-        const float s = row_scale<false>(a);
+        float s, inv;
+        row_scale<false>(a, s, inv);
         if ((c & 15) == 0) static_cast<float*>(p.scale)[(size_t)m * (p.N / 128) + c / 16] = s;
-        q[c] = row_codes<false>(v[i], s);
+        q[c] = chunk_codes<false>(v[i], s, inv);
       }
     }
   } else {
     // NVFP4: a 16-element block is two neighbouring threads' chunks
     uint32_t* q = reinterpret_cast<uint32_t*>(p.q + (size_t)m * (p.N / 2));
     uint8_t* sf = static_cast<uint8_t*>(p.scale);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      const float own = absmax8(v[i]);
+      float t[8];
+#pragma unroll
+      for (int e = 0; e < CH; ++e)
+        if (e == i) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) unpack_f32x2(v[e][j], t[2 * j], t[2 * j + 1]);
+        }
+      const float own = absmax8(t);
       const float a = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, 1));
       if (c < nch) {
         const uint32_t code = cvt_e4m3x2(__fdiv_rn(__fdiv_rn(a, 6.f), g), 0.f) & 0xFF;
         const float d = __fmul_rn(dec_e4m3(code), g);
         uint32_t packed = 0;
         if (d != 0.f) {
-          float t[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) t[j] = __fdiv_rn(v[i][j], d);
+          for (int j = 0; j < 8; ++j) t[j] = __fdiv_rn(t[j], d);
           packed = cvt_e2m1x8(t);
         }
         q[c] = packed;
@@ -237,9 +251,10 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t st, bool pdl) {
   // NVFP4 also writes the scale rows that pad the last 128-row atom
   const int rows = p.q != nullptr && p.format == QG_NVFP4 ? (p.M + 127) / 128 * 128 : p.M;
   auto threads = [&](int ch) { return ((nch + ch - 1) / ch + 31) / 32 * 32; };
+  // few rows: the shortest chain, a chunk a thread
   if (threads(1) <= 1024 && p.M <= 2 * 148) return launch_ch<1>(p, rows, threads(1), st, pdl);
-  if (threads(2) <= 256) return launch_ch<2>(p, rows, threads(2), st, pdl);
-  if (threads(4) <= 1024) return launch_ch<4>(p, rows, threads(4), st, pdl);
+  if (threads(2) <= 128) return launch_ch<2>(p, rows, threads(2), st, pdl);
+  if (threads(4) <= 512) return launch_ch<4>(p, rows, threads(4), st, pdl);
   return launch_ch<8>(p, rows, threads(8), st, pdl);
 }
 

@@ -4,29 +4,91 @@
 // are 0, so that it reads back as NaN and its codes stay finite (a cached row
 // that a mask hides must not reach a sum: 0 * code is 0, 0 * NaN is not).
 #pragma once
+#include "ptx.cuh"
 #include "quant_math.cuh"
 
 namespace qg {
 
-// Maximum of the magnitudes' bit patterns: ordered like the magnitudes, with
-// infinity and NaN above every finite value.
-__device__ __forceinline__ uint32_t absmax_bits8(const float (&x)[8]) {
-  uint32_t m = 0;
+// Eight fp32 values as four packed pairs (the two-wide arithmetic of sm_100).
+using Chunk = uint64_t[4];
+__device__ __forceinline__ void unpack_chunk(const uint4& v, Chunk& x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-  return m;
+  for (int i = 0; i < 4; ++i)
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x[i]) : "r"(w[i] << 16), "r"(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 pack_chunk(const Chunk& x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack_f32x2(x[i], a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool INT8>
-__device__ __forceinline__ float row_scale(uint32_t amax_bits) {
-  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-  return scale_of_amax<INT8>(__uint_as_float(amax_bits));
+// The larger magnitude, NaN if either is NaN (fmaxf would drop it); the sign
+// is of no meaning.
+__device__ __forceinline__ float absmax_nan(float m, float x) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(x));
+  return r;
+}
+__device__ __forceinline__ float absmax_chunk(const Chunk& x) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack_f32x2(x[i], a, b);
+    m[i] = absmax_nan(a, b);
+  }
+  return absmax_nan(absmax_nan(m[0], m[1]), absmax_nan(m[2], m[3]));
 }
 
+// Scale of a row, and its reciprocal.  Codes are x * (1 / scale) rounded, not
+// x / scale: the product is within 2^-22.9 of the quotient, so a code differs
+// only where the quotient is that near to a border between two codes, and the
+// division was a third of the norm's instructions (16384 x 5120: see norm.cu).
 template <bool INT8>
-__device__ __forceinline__ uint2 row_codes(const float (&x)[8], float s) {
+__device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
+  amax = fabsf(amax);
+  if (!(amax <= 3.402823466e38f)) {
+    s = __uint_as_float(0x7fc00000u);
+    inv = 0.f;
+  } else {
+    s = scale_of_amax<INT8>(amax);
+    // s = 0 only below 448 times the least fp32 number: such a row's codes are 0
+    inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+    if (inv > 3.402823466e38f) inv = 0.f;
+  }
+}
+
+// Codes of 8 values, low byte first; all zero for a row whose scale is NaN.
+template <bool INT8>
+__device__ __forceinline__ uint2 chunk_codes(const Chunk& x, float s, float inv) {
   if (s != s) return make_uint2(0u, 0u);
-  return quant8<INT8>(x, s);
+  const uint64_t k = pack_f32x2(inv, inv);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float a, b, c, d;
+    unpack_f32x2(mul_f32x2(x[2 * h], k), a, b);
+    unpack_f32x2(mul_f32x2(x[2 * h + 1], k), c, d);
+    if constexpr (INT8) {
+      // |x| inv <= 127 (1 + 2^-22): nothing to clamp but the pack's own range
+      const int q[4] = {__float2int_rn(a), __float2int_rn(b), __float2int_rn(c), __float2int_rn(d)};
+      uint32_t r;
+      asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\tcvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+          : "=r"(r)
+          : "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]));
+      w[h] = r;
+    } else {
+      w[h] = cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
+    }
+  }
+  return make_uint2(w[0], w[1]);
 }
 
 // Byte offset of scale (r, c) in the 128x4 tiled NVFP4 layout of C columns.
