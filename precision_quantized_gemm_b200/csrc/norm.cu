@@ -31,25 +31,39 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum / unsigned maximum over the CTA, the same in every thread.  Each call
-// of a row takes its own 32 words of `red`, so one barrier is enough.
-__device__ __forceinline__ float cta_sum(float v, float* red) {
-  v = warp_sum(v);
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+// Sum / maximum over the CTA, the same in every thread.  Each call of a row
+// takes its own 36 words of `red`, so one barrier is enough; the warps'
+// partials are read four at a time (the last warp zeroes the fours' rest),
+// which is a shorter chain than a second round of shuffles.
+__device__ __forceinline__ void partial(float v, float* red) {
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (l == 0) red[w] = v;
+  else if (w == warps - 1 && l < 4) red[w + l] = 0.f;
   __syncthreads();
-  return warp_sum(l < (int)(blockDim.x >> 5) ? red[l] : 0.f);
 }
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  if (l == 0) red[w] = v;
-  __syncthreads();
-  return __reduce_max_sync(0xffffffffu, l < (int)(blockDim.x >> 5) ? red[l] : 0u);
+__device__ __forceinline__ float cta_sum(float v, float* red) {
+  partial(warp_sum(v), red);
+  float s = 0.f;
+  for (int i = 0; i < (int)(blockDim.x >> 5); i += 4) {
+    const float4 p = *reinterpret_cast<const float4*>(red + i);
+    s += (p.x + p.y) + (p.z + p.w);
+  }
+  return s;
+}
+// Of magnitudes, NaN kept: their bit patterns are ordered like them, NaN last.
+__device__ __forceinline__ float cta_absmax(float v, float* red) {
+  partial(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu)), red);
+  float m = 0.f;
+  for (int i = 0; i < (int)(blockDim.x >> 5); i += 4) {
+    const float4 p = *reinterpret_cast<const float4*>(red + i);
+    m = absmax_nan(absmax_nan(m, absmax_nan(p.x, p.y)), absmax_nan(p.z, p.w));
+  }
+  return m;
 }
 
 // x <- norm(x) * (w + offset) + b over the row's `nch` chunks.
-template <int CH>
+// FULL: every thread has all CH chunks.
+template <int CH, bool FULL>
 __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, bool layer, float eps,
                                          const uint4* __restrict__ w, const uint4* __restrict__ b, float offset,
                                          float* red) {
@@ -65,7 +79,7 @@ __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, b
     const uint64_t m = pack_f32x2(-mean, -mean);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const bool in = threadIdx.x + i * blockDim.x < nch;
+      const bool in = FULL || threadIdx.x + i * blockDim.x < nch;
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[i][j] = in ? add_f32x2(x[i][j], m) : 0ull;
     }
@@ -77,12 +91,12 @@ __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, b
     for (int j = 0; j < 4; ++j) q = fma_f32x2(x[i][j], x[i][j], q);
   float a, c;
   unpack_f32x2(q, a, c);
-  const float r = rsqrtf(cta_sum(a + c, red + 32) * inv_n + eps);
+  const float r = rsqrtf(cta_sum(a + c, red + 36) * inv_n + eps);
   const uint64_t r2 = pack_f32x2(r, r), o2 = pack_f32x2(offset, offset);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int at = threadIdx.x + i * blockDim.x;
-    if (at < nch) {
+    if (FULL || at < nch) {
       Chunk v;
       unpack_chunk(__ldg(w + at), v);
       if (offset != 0.f) {
@@ -100,9 +114,9 @@ __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, b
   }
 }
 
-template <int CH>
-__global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormParams p) {
-  __shared__ float red[160];
+template <int CH, bool FULL>
+__global__ void __launch_bounds__(CH == 1 ? 1024 : 512, CH == 4 ? 2 : 1) norm_kernel(const NormParams p) {
+  __shared__ __align__(16) float red[5 * 36];
   griddep_launch_dependents();
   griddep_wait();
   const int m = blockIdx.x;
@@ -127,20 +141,20 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormPa
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    rv[i] = rr && c < nch ? rr[c] : zero;
-    xv[i] = xr && c < nch ? xr[c] : zero;
+    rv[i] = rr && (FULL || c < nch) ? rr[c] : zero;
+    xv[i] = xr && (FULL || c < nch) ? xr[c] : zero;
   }
   Chunk v[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) unpack_chunk(xv[i], v[i]);
   if (p.post_norm)
-    norm_row<CH>(v, nch, p.inv_n, p.post_norm == QG_NORM_LAYER, p.eps, p.post_weight, p.post_bias, p.weight_offset,
+    norm_row<CH, FULL>(v, nch, p.inv_n, p.post_norm == QG_NORM_LAYER, p.eps, p.post_weight, p.post_bias, p.weight_offset,
                  red);
   const uint64_t bs = pack_f32x2(p.block_scale, p.block_scale), rs = pack_f32x2(p.residual_scale, p.residual_scale);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    if (gr != nullptr && c < nch) {
+    if (gr != nullptr && (FULL || c < nch)) {
       Chunk gv;
       unpack_chunk(gr[c], gv);
 #pragma unroll
@@ -150,16 +164,16 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormPa
     unpack_chunk(rv[i], r);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[i][j] = fma_f32x2(rs, r[j], mul_f32x2(bs, v[i][j]));
-    if (p.h != nullptr && c < nch) reinterpret_cast<uint4*>(p.h + (size_t)m * p.ldh)[c] = pack_chunk(v[i]);
+    if (p.h != nullptr && (FULL || c < nch)) reinterpret_cast<uint4*>(p.h + (size_t)m * p.ldh)[c] = pack_chunk(v[i]);
   }
   if (!p.pre_norm) return;
-  norm_row<CH>(v, nch, p.inv_n, p.pre_norm == QG_NORM_LAYER, p.eps, p.pre_weight, p.pre_bias, p.weight_offset,
-               red + 64);
+  norm_row<CH, FULL>(v, nch, p.inv_n, p.pre_norm == QG_NORM_LAYER, p.eps, p.pre_weight, p.pre_bias, p.weight_offset,
+               red + 72);
   if (p.y != nullptr) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nch) reinterpret_cast<uint4*>(p.y + (size_t)m * p.ldy)[c] = pack_chunk(v[i]);
+      if ((FULL || c < nch)) reinterpret_cast<uint4*>(p.y + (size_t)m * p.ldy)[c] = pack_chunk(v[i]);
     }
   }
   if (p.q == nullptr) return;
@@ -167,8 +181,7 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormPa
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) a = absmax_nan(a, absmax_chunk(v[i]));
-    // magnitudes' bit patterns are ordered like them, NaN last
-    a = __uint_as_float(cta_max(__float_as_uint(a) & 0x7fffffffu, reinterpret_cast<uint32_t*>(red + 128)));
+    a = cta_absmax(a, red + 144);
     const bool int8 = p.format == QG_W8A8_INT8;
     float s, inv;
     if (int8) row_scale<true>(a, s, inv);
@@ -178,7 +191,7 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormPa
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nch) q[c] = int8 ? chunk_codes<true>(v[i], s, inv) : chunk_codes<false>(v[i], s, inv);
+      if ((FULL || c < nch)) q[c] = int8 ? chunk_codes<true>(v[i], s, inv) : chunk_codes<false>(v[i], s, inv);
     }
   } else if (p.format == QG_BLOCK_FP8) {
     // a 128-element group is 16 chunks, held by 16 neighbouring threads
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormPa
       float a = absmax_chunk(v[i]);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = absmax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-      if (c < nch) {
+      if ((FULL || c < nch)) {
         float s, inv;
         row_scale<false>(a, s, inv);
         if ((c & 15) == 0) static_cast<float*>(p.scale)[(size_t)m * (p.N / 128) + c / 16] = s;
@@ -213,7 +226,7 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormPa
         }
       const float own = absmax8(t);
       const float a = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, 1));
-      if (c < nch) {
+      if ((FULL || c < nch)) {
         const uint32_t code = cvt_e4m3x2(__fdiv_rn(__fdiv_rn(a, 6.f), g), 0.f) & 0xFF;
         const float d = __fmul_rn(dec_e4m3(code), g);
         uint32_t packed = 0;
@@ -241,7 +254,7 @@ cudaError_t launch_ch(const NormParams& p, int rows, int threads, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, norm_kernel<CH>, p);
+  return cudaLaunchKernelEx(&cfg, p.N == threads * CH * 8 ? norm_kernel<CH, true> : norm_kernel<CH, false>, p);
 }
 
 }  // namespace
