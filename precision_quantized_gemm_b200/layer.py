@@ -18,11 +18,12 @@ the caller's to order, as with any torch operation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from collections import namedtuple
 
-from . import (FORMATS, NORM_KINDS, QG_FP8_DYNAMIC, QG_NORM_NONE, QG_W8A8_INT8, QGEMM_ATTEND_MAX_Q, Operand, Workspace,
-               _torch, check, lib, qg_attend, qg_cache, qg_cache_write, qg_norm)
+from . import (NORM_KINDS, QG_NORM_NONE, QG_NVFP4, QGEMM_ATTEND_MAX_Q, Operand, Workspace, _torch, check, lib, qg_attend,
+               qg_cache, qg_cache_write, qg_norm, qg_operand, qgemm_operand_bytes)
 
 __all__ = ["Cache", "NormResult", "Rope", "attend", "cache_read", "cache_write", "norm", "rope_frequencies"]
 
@@ -60,36 +61,37 @@ def qgemm_attend(cache, a, ws_ptr, ws_bytes, stream):
 
 
 # ------------------------------------------------------------------- checking --
-class _On:
-    """Makes a tensor's device and the launch stream current, where they are not."""
+torch = None  # imported at the first call, as in the package's own module
 
-    __slots__ = ("dev", "stream", "ctx")
 
-    def __init__(self, device, stream):
-        self.dev, self.stream, self.ctx = device, stream, None
+def _ready(device, stream) -> bool:
+    """Whether the launch goes where the caller stands: the current stream of
+    the current device, which is the tensors'.  (The raw accessors cost a
+    tenth of torch.cuda.current_stream(), half of a small call.)"""
+    global torch
+    if torch is None:
+        torch = _torch()
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    return stream is None and device.index == torch._C._cuda_getDevice()
 
-    def __enter__(self):
-        cuda = _torch().cuda
-        if self.dev.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        if self.stream is not None:
-            if self.stream.device != self.dev:
-                raise ValueError("the stream is not one of the tensors' device")
-            self.ctx = cuda.stream(self.stream)
-            self.ctx.__enter__()
-        elif self.dev.index != cuda.current_device():
-            self.ctx = cuda.device(self.dev)
-            self.ctx.__enter__()
-        return (self.stream or cuda.current_stream()).cuda_stream
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _there(device, stream):
+    """Makes the tensors' device and the stream to launch on current."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("the stream is not one of the tensors' device")
+    return torch.cuda.stream(stream)
+
+
+def _here(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _rows(name, t, rows, width, device):
     """A bf16 matrix [rows, width] with contiguous rows; its row stride."""
-    if t.dtype != _torch().bfloat16 or t.shape != (rows, width) or t.device != device:
+    if t.dtype != torch.bfloat16 or t.shape != (rows, width) or t.device != device:
         raise ValueError(f"{name}: bf16 [{rows}, {width}] on {device} wanted")
     if width > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: rows must be contiguous")
@@ -98,7 +100,7 @@ def _rows(name, t, rows, width, device):
 
 def _heads(name, t, tokens, heads, dim, device):
     """A bf16 tensor [tokens, heads, dim] whose heads lie side by side; its token stride."""
-    if t.dtype != _torch().bfloat16 or t.shape != (tokens, heads, dim) or t.device != device:
+    if t.dtype != torch.bfloat16 or t.shape != (tokens, heads, dim) or t.device != device:
         raise ValueError(f"{name}: bf16 [{tokens}, {heads}, {dim}] on {device} wanted")
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
@@ -107,7 +109,7 @@ def _heads(name, t, tokens, heads, dim, device):
 
 
 def _ints(name, t, shape, device, dtype=None):
-    dtype = dtype or _torch().int32
+    dtype = dtype or torch.int32
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {device} wanted")
     return t.data_ptr()
@@ -116,7 +118,7 @@ def _ints(name, t, shape, device, dtype=None):
 def _vector(name, t, width, device):
     if t is None:
         return None
-    if t.dtype != _torch().bfloat16 or t.shape != (width,) or t.device != device or not t.is_contiguous():
+    if t.dtype != torch.bfloat16 or t.shape != (width,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous bf16 [{width}] on {device} wanted")
     return t.data_ptr()
 
@@ -135,52 +137,80 @@ def norm(residual, weight, x=None, *, bias=None, kind="rms", post_weight=None, p
     ``h`` / ``y``: bf16 [M, N] buffers for them; h is also returned when x is
     given or nothing else is asked for, and may be ``residual`` (in place).
     NVFP4 needs ``static_amax``.  Returns NormResult(h, y, operand)."""
-    torch = _torch()
     first = residual if residual is not None else x
     if first is None or first.dim() != 2:
         raise ValueError("residual or x: bf16 [M, N] wanted")
-    if kind not in ("rms", "layer"):
+    code = NORM_KINDS.get(kind, QG_NORM_NONE)
+    if code == QG_NORM_NONE:
         raise ValueError("kind is 'rms' or 'layer'")
-    M, N = first.shape
-    dev = first.device
     if weight is None and (fmt is not None or out is not None or y is not None):
         raise ValueError("y needs a weight")
     if out is not None and fmt is None:
         fmt = out.fmt
     if out is not None and (out.fmt != fmt or out.is_weight):
         raise ValueError("out is not an activation operand of this format")
-    code = NORM_KINDS[kind]
-    with _On(dev, stream) as st:
-        if h is None and (x is not None or weight is None):
-            h = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-        if weight is not None and fmt is None and y is None:
-            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-        if fmt is not None and out is None:
-            out = Operand(fmt, False, M, N, dev)
-        a = qg_norm()
-        for name, t, ld in (("residual", residual, "ldr"), ("x", x, "ldx"), ("h", h, "ldh"), ("y", y, "ldy")):
-            if t is not None:
-                setattr(a, ld, _rows(name, t, M, N, dev))
-                setattr(a, name, t.data_ptr())
-        if gate is not None:
-            if gate.dim() == 1:
-                a.gate = _vector("gate", gate, N, dev)
-            else:
-                a.ldg = _rows("gate", gate, M, N, dev)
-                a.gate = gate.data_ptr()
-        a.pre_weight, a.pre_bias = _vector("weight", weight, N, dev), _vector("bias", bias, N, dev)
-        a.post_weight, a.post_bias = _vector("post_weight", post_weight, N, dev), _vector("post_bias", post_bias, N, dev)
-        a.pre_norm = code if weight is not None else QG_NORM_NONE
-        a.post_norm = code if post_weight is not None else QG_NORM_NONE
-        a.residual_scale, a.block_scale, a.eps, a.weight_offset = residual_scale, block_scale, eps, weight_offset
-        amax = None
-        if static_amax is not None:
-            if static_amax.dtype != torch.float32 or static_amax.numel() != 1 or static_amax.device != dev:
-                raise ValueError(f"static_amax: one fp32 value on {dev} wanted")
-            amax = static_amax.data_ptr()
-        check(lib().qgemm_norm(a, M, N, fmt if fmt is not None else 0, out.c if out is not None else None, amax, st),
-              "qgemm_norm")
+    M, N = first.shape
+    dev = first.device
+    if not _ready(dev, stream):
+        with _there(dev, stream):
+            return norm(residual, weight, x, bias=bias, kind=kind, post_weight=post_weight, post_bias=post_bias,
+                        gate=gate, block_scale=block_scale, residual_scale=residual_scale, eps=eps,
+                        weight_offset=weight_offset, fmt=fmt, out=out, h=h, y=y, static_amax=static_amax)
+    if h is None and (x is not None or weight is None):
+        h = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    if weight is not None and fmt is None and y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    if fmt is not None and out is None:
+        out = _operand(fmt, M, N, dev)
+    a = qg_norm(residual_scale=residual_scale, block_scale=block_scale, eps=eps, weight_offset=weight_offset)
+    if residual is not None:
+        a.ldr, a.residual = _rows("residual", residual, M, N, dev), residual.data_ptr()
+    if x is not None:
+        a.ldx, a.x = _rows("x", x, M, N, dev), x.data_ptr()
+    if h is not None:
+        a.ldh, a.h = _rows("h", h, M, N, dev), h.data_ptr()
+    if y is not None:
+        a.ldy, a.y = _rows("y", y, M, N, dev), y.data_ptr()
+    if gate is not None:
+        if gate.dim() == 1:
+            a.gate = _vector("gate", gate, N, dev)
+        else:
+            a.ldg, a.gate = _rows("gate", gate, M, N, dev), gate.data_ptr()
+    if weight is not None:
+        a.pre_norm, a.pre_weight = code, _vector("weight", weight, N, dev)
+    if bias is not None:
+        a.pre_bias = _vector("bias", bias, N, dev)
+    if post_weight is not None:
+        a.post_norm, a.post_weight = code, _vector("post_weight", post_weight, N, dev)
+    if post_bias is not None:
+        a.post_bias = _vector("post_bias", post_bias, N, dev)
+    amax = None
+    if static_amax is not None:
+        if static_amax.dtype != torch.float32 or static_amax.numel() != 1 or static_amax.device != dev:
+            raise ValueError(f"static_amax: one fp32 value on {dev} wanted")
+        amax = static_amax.data_ptr()
+    check(lib().qgemm_norm(a, M, N, fmt if fmt is not None else 0, out.c if out is not None else None, amax, _here(dev)),
+          "qgemm_norm")
     return NormResult(h, y, out)
+
+
+@functools.lru_cache(maxsize=1024)
+def _operand_bytes(fmt, M, N):
+    return qgemm_operand_bytes(fmt, False, M, N)
+
+
+def _operand(fmt, M, N, dev):
+    """An activation operand that the norm fills: nothing to clear beforehand,
+    and a tensor scale for NVFP4 only."""
+    qb, sb = _operand_bytes(fmt, M, N)
+    o = Operand.__new__(Operand)
+    o.fmt, o.is_weight, o.rows, o.K = fmt, False, M, N
+    o.q = torch.empty(qb, dtype=torch.uint8, device=dev)
+    o.scale = torch.empty(sb, dtype=torch.uint8, device=dev)
+    o.global_scale = torch.empty(4, dtype=torch.float32, device=dev) if fmt == QG_NVFP4 else None
+    o.c = qg_operand(o.q.data_ptr(), o.scale.data_ptr(),
+                     o.global_scale.data_ptr() if fmt == QG_NVFP4 else None, M, N)
+    return o
 
 
 # ----------------------------------------------------------------------- rope --
@@ -275,45 +305,46 @@ def cache_write(cache: Cache, k, v, slots, q=None, rope: Rope | None = None, pos
     not written; the others must differ), rotating keys by ``rope`` at
     ``positions`` (int32 [T]).  ``q`` (bf16 [T, q_heads, head_dim]) is rotated
     alongside into ``q_out`` (allocated if None, may be q), which is returned."""
-    torch = _torch()
     if k.dim() != 3:
         raise ValueError("k: bf16 [tokens, kv_heads, head_dim] wanted")
     T, dev, D = k.shape[0], cache.device, cache.head_dim
-    with _On(dev, stream) as st:
-        a = qg_cache_write()
-        a.ldk, a.ldv = _heads("k", k, T, cache.kv_heads, D, dev), _heads("v", v, T, cache.kv_heads, D, dev)
-        a.k, a.v, a.slots = k.data_ptr(), v.data_ptr(), _ints("slots", slots, (T,), dev)
-        if q is not None:
-            if q.dim() != 3:
-                raise ValueError("q: bf16 [tokens, q_heads, head_dim] wanted")
-            a.q_heads = q.shape[1]
-            if q_out is None:
-                q_out = torch.empty(T, a.q_heads, D, dtype=torch.bfloat16, device=dev)
-            a.ldq, a.ldqo = _heads("q", q, T, a.q_heads, D, dev), _heads("q_out", q_out, T, a.q_heads, D, dev)
-            a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        if rope is not None:
-            if positions is None or rope.frequency.device != dev:
-                raise ValueError(f"a rope needs positions, and its frequency on {dev}")
-            a.positions, a.frequency = _ints("positions", positions, (T,), dev), rope.frequency.data_ptr()
-            a.rope_dim, a.interleaved, a.magnitude = rope.dim, rope.interleaved, rope.magnitude
-        check(lib().qgemm_cache_write(cache.c, a, T, st), "qgemm_cache_write")
+    if not _ready(dev, stream):
+        with _there(dev, stream):
+            return cache_write(cache, k, v, slots, q=q, rope=rope, positions=positions, q_out=q_out)
+    a = qg_cache_write(ldk=_heads("k", k, T, cache.kv_heads, D, dev), ldv=_heads("v", v, T, cache.kv_heads, D, dev),
+                       k=k.data_ptr(), v=v.data_ptr(), slots=_ints("slots", slots, (T,), dev))
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q: bf16 [tokens, q_heads, head_dim] wanted")
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        a.q_heads, a.ldq, a.ldqo = Hq, _heads("q", q, T, Hq, D, dev), _heads("q_out", q_out, T, Hq, D, dev)
+        a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if rope is not None:
+        if positions is None or rope.frequency.device != dev:
+            raise ValueError(f"a rope needs positions, and its frequency on {dev}")
+        a.positions, a.frequency = _ints("positions", positions, (T,), dev), rope.frequency.data_ptr()
+        a.rope_dim, a.interleaved, a.magnitude = rope.dim, rope.interleaved, rope.magnitude
+    check(lib().qgemm_cache_write(cache.c, a, T, _here(dev)), "qgemm_cache_write")
     return q_out
 
 
 def cache_read(cache: Cache, slots, k=None, v=None, stream=None):
     """Keys and values of ``slots`` (int32 [T]; below 0: a zero row) as bf16
     [T, kv_heads, head_dim]; returns (k, v)."""
-    torch = _torch()
     T, dev = slots.shape[0], cache.device
-    with _On(dev, stream) as st:
-        shape = (T, cache.kv_heads, cache.head_dim)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-        check(lib().qgemm_cache_read(cache.c, _ints("slots", slots, (T,), dev), T, k.data_ptr(),
-                                     _heads("k", k, *shape, dev), v.data_ptr(), _heads("v", v, *shape, dev), st),
-              "qgemm_cache_read")
+    if not _ready(dev, stream):
+        with _there(dev, stream):
+            return cache_read(cache, slots, k=k, v=v)
+    shape = (T, cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    check(lib().qgemm_cache_read(cache.c, _ints("slots", slots, (T,), dev), T, k.data_ptr(),
+                                 _heads("k", k, *shape, dev), v.data_ptr(), _heads("v", v, *shape, dev), _here(dev)),
+          "qgemm_cache_read")
     return k, v
 
 
@@ -331,30 +362,31 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
     default head_dim ** -0.5.  lse: fp32 [T, q_heads] buffer for the log sums.
     Returns out (bf16
     [T, q_heads, head_dim]); rows that belong to no sequence are not written."""
-    torch = _torch()
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("q: bf16 [tokens, q_heads, head_dim], page_table: int32 [batch, max_pages] wanted")
     T, Hq, D = q.shape
     B, pages = page_table.shape
     dev = cache.device
-    with _On(dev, stream) as st:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
-        a = qg_attend()
-        a.ldq, a.ldo = _heads("q", q, T, Hq, cache.head_dim, dev), _heads("out", out, T, Hq, D, dev)
-        a.q, a.out = q.data_ptr(), out.data_ptr()
-        a.q_offsets, a.kv_len = _ints("q_offsets", q_offsets, (B + 1,), dev), _ints("kv_len", kv_len, (B,), dev)
-        a.page_table = _ints("page_table", page_table, (B, pages), dev)
-        if lse is not None:
-            a.lse = _ints("lse", lse, (T, Hq), dev, torch.float32)
-        if tree_mask is not None:
-            if tree_mask.dim() != 2:
-                raise ValueError("tree_mask: int64 [tokens, words] wanted")
-            a.mask_words = tree_mask.shape[1]
-            a.tree_mask = _ints("tree_mask", tree_mask, (T, a.mask_words), dev, torch.int64)
-        a.q_heads, a.batch, a.tokens, a.max_pages = Hq, B, T, pages
-        a.max_q = min(T, QGEMM_ATTEND_MAX_Q) if max_q is None else max_q
-        a.scale = D ** -0.5 if scale is None else scale
-        workspace = workspace or Workspace(dev)
-        wsp, wsb = workspace.get(lib().qgemm_attend_workspace_size(cache.c, a))
-        check(lib().qgemm_attend(cache.c, a, wsp, wsb, st), "qgemm_attend")
+    if not _ready(dev, stream):
+        with _there(dev, stream):
+            return attend(cache, q, q_offsets, kv_len, page_table, tree_mask=tree_mask, scale=scale, max_q=max_q,
+                          out=out, lse=lse, workspace=workspace)
+    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
+    a = qg_attend(ldq=_heads("q", q, T, Hq, cache.head_dim, dev), ldo=_heads("out", out, T, Hq, D, dev),
+                  q=q.data_ptr(), out=out.data_ptr(), q_offsets=_ints("q_offsets", q_offsets, (B + 1,), dev),
+                  kv_len=_ints("kv_len", kv_len, (B,), dev), page_table=_ints("page_table", page_table, (B, pages), dev),
+                  q_heads=Hq, batch=B, tokens=T, max_pages=pages,
+                  max_q=min(T, QGEMM_ATTEND_MAX_Q) if max_q is None else max_q,
+                  scale=D ** -0.5 if scale is None else scale)
+    if lse is not None:
+        a.lse = _ints("lse", lse, (T, Hq), dev, torch.float32)
+    if tree_mask is not None:
+        if tree_mask.dim() != 2:
+            raise ValueError("tree_mask: int64 [tokens, words] wanted")
+        a.mask_words = tree_mask.shape[1]
+        a.tree_mask = _ints("tree_mask", tree_mask, (T, a.mask_words), dev, torch.int64)
+    L = lib()
+    workspace = workspace or Workspace(dev)
+    wsp, wsb = workspace.get(L.qgemm_attend_workspace_size(cache.c, a))
+    check(L.qgemm_attend(cache.c, a, wsp, wsb, _here(dev)), "qgemm_attend")
     return out
