@@ -2,16 +2,21 @@
 // (single tokens and small trees): qg_attend_rows_kernel, the merge of items
 // that span CTAs, and the choice between the kernels.
 //
-// Bound: HBM.  16 rows (the query heads of one key head, times the drafted
-// tokens) read 2 D code bytes and 8 scale bytes per position, 4 x 16 x D
-// flops: 31 flops per byte at most, far below the warp-level MMA's rate.  So
-// the kernel is built to keep loads in flight: every warp streams its own
-// blocks of 32 positions through its own ring (TMA boxes of whole rows with
-// the row-wide swizzle, bulk copies for the scales), with no barrier between
-// warps until the end of an item.  Codes become f16 in registers on their way
-// into mma.sync fragments; the swizzle makes both fragment reads free of bank
-// conflicts (D = 128), and the head's channels are permuted the same way in
-// queries and keys so that a lane reads 16 neighbouring codes at once.
+// Bound: HBM.  8 NR rows (the query heads of one key head, times the drafted
+// tokens) read 2 D code bytes and 8 scale bytes per position: 16 flops per
+// byte and row tile, far below the warp-level MMA's rate.  What is scarce is
+// issue: decoding to f16 takes an instruction per two codes.  So positions are
+// the MMA's 16-row operand and the query rows its 8 columns,
+//   S^T = K Q^T,  O^T = V^T W^T,
+// which for the usual 4 to 8 query heads of a key head halves the MMAs, the
+// exponentials and the registers of the other orientation (64 x 16384
+// positions, 64 query and 8 key heads: 311 us there, 235 us here).
+// Every warp streams its own blocks of 32 positions through its own ring (TMA
+// boxes of whole rows with the row-wide swizzle, bulk copies for the scales),
+// with no barrier between warps until the end of an item.  The swizzle makes
+// both fragment reads free of bank conflicts (D = 128), and the head's
+// channels are permuted the same way in queries and keys so that a lane reads
+// 16 neighbouring codes at once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,21 +32,26 @@
 namespace qg {
 namespace {
 
-constexpr int kRows = 16;     // rows per item
 constexpr int kUnit = 64;     // positions per unit of work
 constexpr int kBlock = 32;    // positions per ring stage of a warp
-constexpr int kWarps = 8;
 constexpr int kStages = 2;
 
-template <int D>
+// Warps per CTA: as many as the registers of NR row tiles leave room for (a
+// warp issues an instruction every four to five cycles).
+template <int NR>
+constexpr int kRowsWarps = NR == 1 ? 12 : 8;
+
+template <int D, int NR>
 struct RowsSmem {
   static constexpr int kCodes = kBlock * D;                  // K or V codes of a stage
-  static constexpr int kStage = 2 * kCodes + 2 * kBlock * 4;  // + K and V scales
-  static constexpr int kStageAlloc = (kStage + 1023) / 1024 * 1024;
-  static constexpr int kRing = kWarps * kStages * kStageAlloc;
+  static constexpr int kStage = 2 * kCodes;
+  static constexpr int kRing = kRowsWarps<NR> * kStages * kStage;
+  static constexpr int kScale = 2 * kBlock * 4;              // K and V scales of a stage
+  static constexpr int kScales = kRowsWarps<NR> * kStages * kScale;
+  static constexpr int kTotal = 1024 + kRing + kScales;
+  // the warps' partial results meet in the ring, empty by then
   static constexpr int kMergeRow = D + 4;                    // floats; spreads rows over banks
-  static constexpr int kMerge = 4 * kRows * kMergeRow * 4;
-  static constexpr int kTotal = 1024 + kRing + kMerge;
+  static_assert(4 * 8 * NR * kMergeRow * 4 <= kRing, "merge buffers fit the ring");
 };
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int row) {
@@ -50,6 +60,11 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
           dst),
       "l"(map), "r"(smem_u32(bar)), "r"(0), "r"(row)
       : "memory");
+}
+__device__ __forceinline__ void bulk_floats(uint32_t dst, const float* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -61,11 +76,23 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ float lds4(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 b16 matrix held as fragments.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -79,23 +106,26 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int D, bool INT8>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+template <int D, bool INT8, int NR>
+__global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
     qg_attend_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                           const AttendParams p) {
-  using S = RowsSmem<D>;
+  using S = RowsSmem<D, NR>;
+  constexpr int WARPS = kRowsWarps<NR>;
+  constexpr int ROWS = 8 * NR;
   constexpr int KS = D / 16;   // MMA steps over the head's channels
-  constexpr int NT = D / 8;    // 8-channel output tiles
+  constexpr int MT = D / 16;   // 16-channel output tiles
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sched sched;
-  __shared__ __align__(8) uint64_t bars[kWarps * kStages];
-  __shared__ float2 vsc[kWarps][kBlock];       // (log2 vs, 1 / vs) of the block in hand
-  __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
+  __shared__ __align__(8) uint64_t bars[WARPS * kStages];
+  __shared__ float4 pos_scale[WARPS][kBlock];  // (key scale, log2 vs, 1 / vs) of the block in hand
+  __shared__ float part_m[WARPS][ROWS], part_l[WARPS][ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t ring = base + warp * kStages * S::kStageAlloc;
-  float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + S::kRing);
+  const uint32_t ring = base + warp * kStages * S::kStage;
+  const uint32_t scale_ring = base + S::kRing + warp * kStages * S::kScale;
+  float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
   uint64_t* bar = bars + warp * kStages;
   if (lane == 0)
     for (int i = 0; i < kStages; ++i) mbar_init(bar + i, 1);
@@ -106,8 +136,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   fence_barrier_init();
   griddep_launch_dependents();
   griddep_wait();
-  const Share share = plan_units(p, kRows, kUnit, sched);
-  if (threadIdx.x == 0) p.records[blockIdx.x] = merge_record(p, sched, share, kRows);
+  const Share share = plan_units(p, ROWS, kUnit, sched);
+  if (threadIdx.x == 0) p.records[blockIdx.x] = merge_record(p, sched, share, ROWS);
   if (blockIdx.x >= share.ctas || share.total == 0) return;
   const int share_begin = share.begin(blockIdx.x), share_end = share.begin(blockIdx.x + 1);
   uint32_t phase = 0;  // bit i: parity of the ring stage's next wait
@@ -115,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
 #pragma unroll 1
   for (int u = share_begin; u < share_end;) {
-    const Piece x = find_piece(p, sched, kRows, u, share_end);
+    const Piece x = find_piece(p, sched, ROWS, u, share_end);
     const int tok0 = sched.tok0[x.seq], len = sched.len[x.seq];
     const int rows = min(sched.n[x.seq], p.max_q) * p.group;
     const int begin = x.unit0 * kUnit, end = min(x.unit1 * kUnit, len);
@@ -133,10 +163,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       return min(max(__ldg(table + (pos >> p.page_shift)), 0), p.pages - 1);
     };
     auto issue = [&](int blk, int page) {
-      const int st = (blk / kWarps) % kStages;
+      const int st = (blk / WARPS) % kStages;
       const int pos0 = begin + blk * kBlock;
       const int live = min((end - pos0 + p.box_rows - 1) / p.box_rows, runs);
-      const uint32_t dst = ring + st * S::kStageAlloc;
+      const uint32_t dst = ring + st * S::kStage;
       if (lane == 0) mbar_arrive_expect_tx(bar + st, live * p.box_rows * (2 * D + 8));
       __syncwarp();
       if (lane < live) {
@@ -144,16 +174,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const int row = (page * p.kv_heads + x.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
         tma_rows(dst + run_off * D, &tmap_k, bar + st, row);
         tma_rows(dst + S::kCodes + run_off * D, &tmap_v, bar + st, row);
-        const uint32_t sc = dst + 2 * S::kCodes + run_off * 4;
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(sc),
-            "l"(p.k_scale + row), "r"(p.box_rows * 4), "r"(smem_u32(bar + st))
-            : "memory");
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                sc + kBlock * 4),
-            "l"(p.v_scale + row), "r"(p.box_rows * 4), "r"(smem_u32(bar + st))
-            : "memory");
+        const uint32_t sc = scale_ring + st * S::kScale + run_off * 4;
+        bulk_floats(sc, p.k_scale + row, p.box_rows * 4, bar + st);
+        bulk_floats(sc + kBlock * 4, p.v_scale + row, p.box_rows * 4, bar + st);
       }
     };
     // the ring is empty between items (a stage's parity carries on); reads and
@@ -166,75 +189,82 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll 1
       for (int i = 0; i < kStages; ++i) {
         if (ahead < nblk) issue(ahead, next_page);
-        ahead += kWarps;
+        ahead += WARPS;
         next_page = page_of(ahead);
       }
     }
 
-    // queries of rows g and g + 8, f16, channels in the order of the key reads
-    uint32_t qa[KS][4];
-    float row_scale[2];
-    int tok[2];       // drafted token of the row, -1 past the last row
+    // query row g of each row tile, f16, channels in the order of the key
+    // reads; scale and drafted token of rows 2 t and 2 t + 1, the lane's score
+    // columns (-1: past the last row)
+    uint32_t qb[NR][KS][2];
+    float power[NR][2];
+    int tok[NR][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = x.row0 + g + 8 * i;
-      const bool live = row < rows;
-      tok[i] = live ? row / p.group : -1;
-      const __nv_bfloat16* src =
-          p.q + (size_t)(tok0 + (live ? tok[i] : 0)) * p.ldq + (x.head * p.group + (live ? row % p.group : 0)) * D;
+    for (int i = 0; i < NR; ++i) {
+      const int row = x.row0 + 8 * i + g;
+      const int mine = row < rows ? row / p.group : -1;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (size_t)(tok0 + max(mine, 0)) * p.ldq + (x.head * p.group + (mine < 0 ? 0 : row - mine * p.group)) * D);
       float amax = 0.f;
-      uint4 raw[D / 32];  // 8 channels each
+      uint32_t raw[KS][2];
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)  // 16-channel chunks t (and t + 4)
 #pragma unroll
         for (int hlf = 0; hlf < 2; ++hlf) {
-          const uint4 v = live ? reinterpret_cast<const uint4*>(src)[(t + 4 * c) * 2 + hlf] : make_uint4(0, 0, 0, 0);
-          raw[c * 2 + hlf] = v;
+          const uint4 v = mine >= 0 ? __ldg(src + (t + 4 * c) * 2 + hlf) : make_uint4(0, 0, 0, 0);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j) {
+            // pair e of the lane's 2 KS pairs: step e / 2, the step's low or high channels
+            const int e = c * 8 + hlf * 4 + j;
+            raw[e >> 1][e & 1] = w[j];
             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+          }
         }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       float up, down;
       row_power(amax, up, down);
-      row_scale[i] = down * p.scale_log2;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t h = f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
-          // pair e of the lane's 2 KS pairs: step e / 2, the step's low or high channels
-          const int e = c * 4 + j;
-          qa[e >> 1][i + 2 * (e & 1)] = h;
-        }
+        for (int e = 0; e < 2; ++e)
+          qb[i][k][e] =
+              f16x2(__uint_as_float(raw[k][e] << 16) * up, __uint_as_float(raw[k][e] & 0xffff0000u) * up);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        power[i][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4) * p.scale_log2;
+        tok[i][e] = __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
       }
     }
 
-    float o[NT][4];
+    // o[i][j]: channels NC g + 2 j (first pair) and the next (second) of row
+    // tile i's rows 2 t, 2 t + 1; NC = D / 8 channels a lane
+    float o[NR][MT][4], m[NR][2], l[NR][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int i = 0; i < NR; ++i) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-    float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+      m[i][0] = m[i][1] = kNegInf;
+      l[i][0] = l[i][1] = 0.f;
+    }
 
-    for (int blk = warp; blk < nblk; blk += kWarps) {
-      const int st = (blk / kWarps) % kStages;
-      const uint32_t kb = ring + st * S::kStageAlloc, vb = kb + S::kCodes, sb = vb + S::kCodes;
+#pragma unroll 1
+    for (int blk = warp; blk < nblk; blk += WARPS) {
+      const int st = (blk / WARPS) % kStages;
+      const uint32_t kb = ring + st * S::kStage, vb = kb + S::kCodes, sb = scale_ring + st * S::kScale;
       const int pos0 = begin + blk * kBlock;
       if (ok) ok = mbar_wait(bar + st, (phase >> st) & 1, p.err, p.wait_ns);
       phase ^= 1u << st;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const bool tail = pos0 + kBlock > end || pos0 + kBlock > past;
       {
-        float vs;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(sb + kBlock * 4 + lane * 4));
         float a, b;
-        value_scale(vs, a, b);
-        vsc[warp][lane] = make_float2(a, b);
+        value_scale(lds4(sb + kBlock * 4 + lane * 4), a, b);
+        pos_scale[warp][lane] = make_float4(lds4(sb + lane * 4), a, b, 0.f);
       }
       if (pos0 + kBlock > end) {
         // rows past the last position hold whatever the page held: an e4m3
@@ -244,88 +274,103 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + r * D + c * 16), "r"(0) : "memory");
       }
       __syncwarp();
-      // scores: 4 tiles of 8 positions
-      float s[4][4];
+      // scores: 2 tiles of 16 positions; a lane has positions 16 mt + g and + 8
+      float s[2][NR][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-        uint32_t w[D / 16];
+        for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint4 v = lds16(kb + chunk_at<D>(nt * 8 + g, t + 4 * c));
-          w[4 * c] = v.x;
-          w[4 * c + 1] = v.y;
-          w[4 * c + 2] = v.z;
-          w[4 * c + 3] = v.w;
-        }
+          for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+        uint32_t w[2][KS];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 v = lds16(kb + chunk_at<D>(mt * 16 + h * 8 + g, t + 4 * c));
+            w[h][4 * c] = v.x;
+            w[h][4 * c + 1] = v.y;
+            w[h][4 * c + 2] = v.z;
+            w[h][4 * c + 3] = v.w;
+          }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          uint32_t b0, b1;
-          decode4<INT8>(w[k], b0, b1);
-          mma16816(s[nt], qa[k], b0, b1);
+          uint32_t a0, a1, a2, a3;
+          decode4<INT8>(w[0][k], a0, a2);
+          decode4<INT8>(w[1][k], a1, a3);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) mma16816(s[mt][i], a0, a1, a2, a3, qb[i][k][0], qb[i][k][1]);
         }
       }
-      float top[2] = {m[0], m[1]};
-      float2 sc[4][2];
-      uint32_t see[2] = {0, 0};  // bits of the block's positions from this lane's first on
-      if (tail) {
+      float4 sc[2][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) see[r] = (uint32_t)(seen_bits(p, tok0, tok[r], end - pos0, past - pos0) >> (2 * t));
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) sc[mt][h] = pos_scale[warp][mt * 16 + h * 8 + g];
+      const bool tail = pos0 + kBlock > end || pos0 + kBlock > past;
+      bool grown = false;
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t see = 0xffffffffu;  // bits of the block's positions from this lane's first on
+          if (tail) see = (uint32_t)(seen_bits(p, tok0, tok[i][e], end - pos0, past - pos0) >> g);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& v = s[mt][i][2 * h + e];
+              v = fmaf(v * power[i][e], sc[mt][h].x, sc[mt][h].y);
+              if (tail && !((see >> (mt * 16 + h * 8)) & 1)) v = kNegInf;
+              grown |= v > m[i][e] + kRescaleAt;  // m = -inf: anything seen
+            }
+        }
+      if (__any_sync(0xffffffffu, grown)) {
+        // a new reference where a row's maximum has passed the old one by more
+        // than 2^8 (weights stay below 256); sums and accumulator follow
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(fmaxf(s[0][i][e], s[0][i][2 + e]), fmaxf(s[1][i][e], s[1][i][2 + e]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const bool up = top > m[i][e] + kRescaleAt;
+            const float f = up ? ex2(m[i][e] - top) : 1.f;  // m = -inf: 0
+            if (up) m[i][e] = top;
+            l[i][e] *= f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              o[i][j][e] *= f;
+              o[i][j][2 + e] *= f;
+            }
+          }
       }
+      uint32_t wb[2][NR][2];  // weights as the second operand of each 16 positions
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        float2 ks;
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks.x), "=f"(ks.y) : "r"(sb + (nt * 8 + 2 * t) * 4));
-        sc[nt][0] = vsc[warp][nt * 8 + 2 * t];
-        sc[nt][1] = vsc[warp][nt * 8 + 2 * t + 1];
+      for (int i = 0; i < NR; ++i) {
+        const float ref[2] = {m[i][0] == kNegInf ? 0.f : m[i][0], m[i][1] == kNegInf ? 0.f : m[i][1]};
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              w[e] = ex2(s[mt][i][2 * h + e] - ref[e]);
+              l[i][e] = fmaf(w[e], sc[mt][h].z, l[i][e]);
+            }
+            wb[mt][i][h] = transpose8x8(f16x2(w[0], w[1]));
+          }
+      }
+      // o^T += codes^T . w^T: a lane reads its 4 positions' codes of channels
+      // [16 g, 16 g + 16) ([8 g, 8 g + 8) for D = 64)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t v[4][D / 32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int e = i & 1, r = i >> 1;
-          s[nt][i] = fmaf(s[nt][i] * row_scale[r], e ? ks.y : ks.x, sc[nt][e].x);
-          if (tail && !((see[r] >> (nt * 8 + e)) & 1)) s[nt][i] = kNegInf;
-          top[r] = fmaxf(top[r], s[nt][i]);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      }
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-        float f[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          f[r] = top[r] > m[r] ? ex2(m[r] - top[r]) : 1.f;  // m = -inf: 0
-          m[r] = top[r];
-          l[r] *= f[r];
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] *= f[i >> 1];
-      }
-      const float mm[2] = {m[0] == kNegInf ? 0.f : m[0], m[1] == kNegInf ? 0.f : m[1]};
-      uint32_t pa[2][4];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = ex2(s[nt][i] - mm[i >> 1]);
-          l[i >> 1] = fmaf(w[i], sc[nt][i & 1].y, l[i >> 1]);
-        }
-        pa[nt >> 1][(nt & 1) * 2] = f16x2(w[0], w[1]);
-        pa[nt >> 1][(nt & 1) * 2 + 1] = f16x2(w[2], w[3]);
-      }
-      // o += w . codes: 2 steps of 16 positions; a lane reads its 4 positions'
-      // codes of channels [16 g, 16 g + 16) ([8 g, 8 g + 8) for D = 64)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t v[4][NT / 4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = k * 16 + (i >> 1) * 8 + 2 * t + (i & 1);
+          const int r = mt * 16 + (i >> 1) * 8 + 2 * t + (i & 1);
           if constexpr (D == 128) {
             const uint4 q = lds16(vb + chunk_at<D>(r, g));
             v[i][0] = q.x;
@@ -339,16 +384,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           }
         }
 #pragma unroll
-        for (int w = 0; w < NT / 4; ++w) {
-          // bytes of two positions side by side: channels 0, 1 then 2, 3
-          uint32_t b0[4], b1[4];
-          decode4<INT8>(__byte_perm(v[0][w], v[1][w], 0x5140), b0[0], b0[1]);
-          decode4<INT8>(__byte_perm(v[0][w], v[1][w], 0x7362), b0[2], b0[3]);
-          decode4<INT8>(__byte_perm(v[2][w], v[3][w], 0x5140), b1[0], b1[1]);
-          decode4<INT8>(__byte_perm(v[2][w], v[3][w], 0x7362), b1[2], b1[3]);
+        for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma16816(o[4 * w + j], pa[k], b0[j], b1[j]);
-        }
+          for (int h = 0; h < 2; ++h) {
+            // bytes of two positions side by side: channels 4 w + 2 h and the next
+            const uint32_t sel = h ? 0x7362 : 0x5140;
+            uint32_t a0, a1, a2, a3;
+            decode4<INT8>(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
+            decode4<INT8>(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) mma16816(o[i][2 * w + h], a0, a1, a2, a3, wb[mt][i][0], wb[mt][i][1]);
+          }
       }
       __syncwarp();
       if (ahead < nblk) {
@@ -356,7 +402,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         // before the copies that refill it
         fence_proxy_async_smem();
         issue(ahead, next_page);
-        ahead += kWarps;
+        ahead += WARPS;
         next_page = page_of(ahead);
       }
     }
@@ -369,39 +415,43 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
     // the warps' partials meet: maxima, then the scaled sums 4 warps at a time
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (l[r] != l[r]) m[r] = 0.f;  // a NaN row keeps its place in the merges
-      if (t == 0) {
-        part_m[warp][g + 8 * r] = m[r];
-        part_l[warp][g + 8 * r] = l[r];
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], d);
+        if (l[i][e] != l[i][e]) m[i][e] = 0.f;  // a NaN row keeps its place in the merges
+        if (g == 0) {
+          part_m[warp][8 * i + 2 * t + e] = m[i][e];
+          part_l[warp][8 * i + 2 * t + e] = l[i][e];
+        }
       }
-    }
     __syncthreads();
-    float f[2];
+    float f[NR][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float top = kNegInf;
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w][g + 8 * r]);
-      f[r] = m[r] == kNegInf ? 0.f : ex2(m[r] - top);
-    }
+      for (int e = 0; e < 2; ++e) {
+        float top = kNegInf;
 #pragma unroll
-    for (int half = 1; half >= 0; --half) {
-      if (warp / 4 == half) {
-        float* dst = merge + (warp % 4) * kRows * S::kMergeRow;
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, part_m[w][8 * i + 2 * t + e]);
+        f[i][e] = m[i][e] == kNegInf ? 0.f : ex2(m[i][e] - top);
+      }
+#pragma unroll 1
+    for (int turn = WARPS / 4 - 1; turn >= 0; --turn) {
+      if (warp / 4 == turn) {
+        float* dst = merge + (warp % 4) * ROWS * S::kMergeRow;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < NR; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int j = 0; j < NT; j += 4) {
-              // o[j][2 r + e]: row g + 8 r, channel NT (2 t + e) + j
-              float4* d4 = reinterpret_cast<float4*>(dst + (g + 8 * r) * S::kMergeRow + NT * (2 * t + e) + j);
-              float4 v = make_float4(o[j][2 * r + e] * f[r], o[j + 1][2 * r + e] * f[r], o[j + 2][2 * r + e] * f[r],
-                                     o[j + 3][2 * r + e] * f[r]);
-              if (half == 0) {
+            for (int j = 0; j < MT; j += 2) {
+              float4* d4 =
+                  reinterpret_cast<float4*>(dst + (8 * i + 2 * t + e) * S::kMergeRow + (D / 8) * g + 2 * j);
+              float4 v = make_float4(o[i][j][e] * f[i][e], o[i][j][2 + e] * f[i][e], o[i][j + 1][e] * f[i][e],
+                                     o[i][j + 1][2 + e] * f[i][e]);
+              if (turn < WARPS / 4 - 1) {
                 const float4 a = *d4;
                 v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
               }
@@ -412,47 +462,44 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     const bool whole = x.unit0 == 0 && x.unit1 == x.units;
     const int slot = 2 * blockIdx.x + (u == share_begin ? 0 : 1);
-    float* part = p.partial + (size_t)slot * kRows * (D + 2);
-    constexpr int TPR = kWarps * 32 / kRows;  // threads per row
-    constexpr int CPT = D / TPR;              // channels per thread
-    const int row = threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * CPT;
-    float top = kNegInf, sum = 0.f;
+    float* part = p.partial + (size_t)slot * ROWS * (D + 2);
+    // 4 channels a thread
+    for (int at = threadIdx.x; at < ROWS * (D / 4); at += WARPS * 32) {
+      const int row = at / (D / 4), c0 = at % (D / 4) * 4;
+      float top = kNegInf, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w][row]);
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, part_m[w][row]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += part_m[w][row] == kNegInf ? 0.f : part_l[w][row] * ex2(part_m[w][row] - top);
-    float acc[CPT];
+      for (int w = 0; w < WARPS; ++w)
+        sum += part_m[w][row] == kNegInf ? 0.f : part_l[w][row] * ex2(part_m[w][row] - top);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      acc[j] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) acc[j] += merge[w * kRows * S::kMergeRow + row * S::kMergeRow + c0 + j];
-    }
-    if (whole) {
-      const int r = x.row0 + row;
-      if (r < rows) {
-        const size_t tk = tok0 + r / p.group;
-        const int h = x.head * p.group + r % p.group;
-        // a row that saw nothing: zeros, and a log-sum of -inf
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        __nv_bfloat162 v[CPT / 2];
-#pragma unroll
-        for (int j = 0; j < CPT / 2; ++j) v[j] = __floats2bfloat162_rn(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-        __nv_bfloat16* dst = p.out + tk * p.ldo + h * D + c0;
-        if constexpr (CPT == 8) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(v);
-        else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(v);
-        if (p.lse != nullptr && c0 == 0)
-          p.lse[tk * p.q_heads + h] = sum == 0.f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+      for (int w = 0; w < 4; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(merge + (w * ROWS + row) * S::kMergeRow + c0);
+        acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < CPT; j += 4)
-        *reinterpret_cast<float4*>(part + row * D + c0 + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-      if (c0 == 0) {
-        part[kRows * D + row] = top;
-        part[kRows * D + kRows + row] = sum;
+      if (whole) {
+        const int r = x.row0 + row;
+        if (r < rows) {
+          const int tk = r / p.group, h = x.head * p.group + r - tk * p.group;
+          // a row that saw nothing: zeros, and a log-sum of -inf
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          __nv_bfloat162 v[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                                 __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+          *reinterpret_cast<uint2*>(p.out + (size_t)(tok0 + tk) * p.ldo + h * D + c0) = *reinterpret_cast<uint2*>(v);
+          if (p.lse != nullptr && c0 == 0)
+            p.lse[(size_t)(tok0 + tk) * p.q_heads + h] =
+                sum == 0.f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+        }
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + c0) = acc;
+        if (c0 == 0) {
+          part[ROWS * D + row] = top;
+          part[ROWS * D + ROWS + row] = sum;
+        }
       }
     }
+    fence_proxy_async_smem();  // the merge buffers become the ring again
     __syncthreads();
     u += x.unit1 - x.unit0;
   }
@@ -534,19 +581,25 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, int threads, size_t smem, void
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-template <int D, bool INT8>
-cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int ctas,
-                        cudaStream_t st, bool pdl) {
+template <int D, bool INT8, int NR>
+cudaError_t launch_rows_nr(const AttendParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int ctas,
+                           cudaStream_t st, bool pdl) {
   static GrowOnlyAttr opened;
-  const void* fn = (const void*)qg_attend_rows_kernel<D, INT8>;
-  constexpr int smem = RowsSmem<D>::kTotal;
+  const void* fn = (const void*)qg_attend_rows_kernel<D, INT8, NR>;
+  constexpr int smem = RowsSmem<D, NR>::kTotal;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const int e = opened.ensure(
       dev, smem, [&](int v) { return (int)cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v); });
   if (e != 0) return (cudaError_t)e;
   void* args[] = {(void*)&tk, (void*)&tv, (void*)&p};
-  return launch_pdl(fn, dim3(ctas), kWarps * 32, smem, args, st, pdl);
+  return launch_pdl(fn, dim3(ctas), kRowsWarps<NR> * 32, smem, args, st, pdl);
+}
+template <int D, bool INT8>
+cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int tile_rows, int ctas,
+                        cudaStream_t st, bool pdl) {
+  return tile_rows == 8 ? launch_rows_nr<D, INT8, 1>(p, tk, tv, ctas, st, pdl)
+                        : launch_rows_nr<D, INT8, 2>(p, tk, tv, ctas, st, pdl);
 }
 
 template <int D, bool INT8>
@@ -567,42 +620,45 @@ cudaError_t launch_tile(const AttendParams& p, const uint8_t* k, const uint8_t* 
 // The rows kernel may leave an item in a part per SM, of few rows: four warps
 // a row.  The tile kernel's items have up to 128 rows: one warp each.
 template <int D>
-cudaError_t launch_merge(const AttendParams& p, bool tiles, int ctas, cudaStream_t st, bool pdl) {
-  int tile_rows = tiles ? kTileRows : kRows;
+cudaError_t launch_merge(const AttendParams& p, int tile_rows, int ctas, cudaStream_t st, bool pdl) {
   void* args[] = {(void*)&p, (void*)&tile_rows};
-  if (tiles)
+  if (tile_rows == kTileRows)
     return launch_pdl((const void*)qg_attend_merge_kernel<D, 16, 1>, dim3(ctas, kTileRows / 16), 512, 0, args, st, pdl);
-  return launch_pdl((const void*)qg_attend_merge_kernel<D, 2, 4>, dim3(ctas, kRows / 2), 256, 0, args, st, pdl);
+  return launch_pdl((const void*)qg_attend_merge_kernel<D, 2, 4>, dim3(ctas, tile_rows / 2), 256, 0, args, st, pdl);
 }
+
+// Rows of an item: the rows kernel takes 8 or 16 and reads the codes once per
+// item, so more rows go to the tile kernel, which reads them once per 128.
+int tile_rows_of(int rows_max) { return rows_max <= 8 ? 8 : rows_max <= 16 ? 16 : kTileRows; }
 
 }  // namespace
 
-// More rows than one 16-row tile read the codes once per 16 rows in the rows
-// kernel; the tile kernel reads them once per 128.
-bool attend_tiles(int rows_max) { return rows_max > kRows; }
+bool attend_tiles(int rows_max) { return tile_rows_of(rows_max) == kTileRows; }
 
 size_t attend_workspace(int head_dim, int rows_max, int sms) {
-  return sizeof(MergeRecord) * sms + (size_t)2 * sms * (attend_tiles(rows_max) ? kTileRows : kRows) * (head_dim + 2) * 4;
+  return sizeof(MergeRecord) * sms + (size_t)2 * sms * tile_rows_of(rows_max) * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
                           const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl) {
-  const bool tiles = attend_tiles(p.max_q * p.group);
+  const int rows = tile_rows_of(p.max_q * p.group);
   p.records = static_cast<MergeRecord*>(workspace);
   p.partial = reinterpret_cast<float*>(p.records + sms);
   cudaError_t e;
-  if (tiles) {
+  if (rows == kTileRows) {
     if (head_dim == 128)
       e = int8 ? launch_tile<128, true>(p, k, v, sms, st, pdl) : launch_tile<128, false>(p, k, v, sms, st, pdl);
     else
       e = int8 ? launch_tile<64, true>(p, k, v, sms, st, pdl) : launch_tile<64, false>(p, k, v, sms, st, pdl);
   } else if (head_dim == 128) {
-    e = int8 ? launch_rows<128, true>(p, *tk, *tv, sms, st, pdl) : launch_rows<128, false>(p, *tk, *tv, sms, st, pdl);
+    e = int8 ? launch_rows<128, true>(p, *tk, *tv, rows, sms, st, pdl)
+             : launch_rows<128, false>(p, *tk, *tv, rows, sms, st, pdl);
   } else {
-    e = int8 ? launch_rows<64, true>(p, *tk, *tv, sms, st, pdl) : launch_rows<64, false>(p, *tk, *tv, sms, st, pdl);
+    e = int8 ? launch_rows<64, true>(p, *tk, *tv, rows, sms, st, pdl)
+             : launch_rows<64, false>(p, *tk, *tv, rows, sms, st, pdl);
   }
   if (e != cudaSuccess) return e;
-  return head_dim == 128 ? launch_merge<128>(p, tiles, sms, st, pdl) : launch_merge<64>(p, tiles, sms, st, pdl);
+  return head_dim == 128 ? launch_merge<128>(p, rows, sms, st, pdl) : launch_merge<64>(p, rows, sms, st, pdl);
 }
 
 }  // namespace qg

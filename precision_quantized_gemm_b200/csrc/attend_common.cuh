@@ -32,6 +32,7 @@ namespace qg {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kVsMin = 7.703719777548943e-34f;  // 2^-110
 constexpr float kVsMax = 3.961408125713217e28f;   // 2^95
+constexpr float kRescaleAt = 8.f;                 // log2: how far a score may pass its row's reference
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -216,11 +217,17 @@ __device__ __forceinline__ unsigned long long seen_bits(const AttendParams& p, i
   return all & (prefix | drafted);
 }
 
-// Scale's log2 and reciprocal with the bounds of the header comment.
+// Scale's log2 and reciprocal with the bounds of the header comment.  log2 is
+// the exponent plus the approximate log2 of the mantissa in [1, 2), whose
+// absolute error is 2^-22 (that of the whole would grow with the exponent).
 __device__ __forceinline__ void value_scale(float vs, float& log2_vs, float& inv_vs) {
-  const float c = fminf(fmaxf(vs, kVsMin), kVsMax);  // NaN -> kVsMin
-  inv_vs = __fdividef(1.f, c);
-  log2_vs = vs - vs == 0.f ? log2f(c) : __uint_as_float(0x7fc00000u);
+  const float c = fminf(fmaxf(vs, kVsMin), kVsMax);  // NaN -> kVsMin; normal
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_vs) : "f"(c));
+  const uint32_t bits = __float_as_uint(c);
+  float lg;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u)));
+  lg += (float)((int)(bits >> 23) - 127);
+  log2_vs = vs - vs == 0.f ? lg : __uint_as_float(0x7fc00000u);
 }
 
 // Power of two that brings a row's largest magnitude to [2^14, 2^15), and its

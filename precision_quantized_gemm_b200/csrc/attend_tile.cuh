@@ -44,7 +44,6 @@ constexpr int kTileRows = 128;
 constexpr int kTilePos = 128;       // positions per tile = unit of work
 constexpr int kTileThreads = 896;
 constexpr int kTileStages = 6;     // descriptors and scales ahead
-constexpr float kRescaleAt = 8.f;   // log2
 
 template <int D>
 struct TileSmem {
