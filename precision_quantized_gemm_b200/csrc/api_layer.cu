@@ -181,6 +181,7 @@ qg_status qgemm_cache_write(const qg_cache* c, const qg_cache_write* w, int toke
   p.slots = w->slots;
   p.positions = w->positions;
   p.frequency = w->frequency;
+  p.tokens = tokens;
   p.ldq = w->ldq;
   p.ldk = w->ldk;
   p.ldv = w->ldv;
@@ -192,7 +193,7 @@ qg_status qgemm_cache_write(const qg_cache* c, const qg_cache_write* w, int toke
   p.page_shift = shift_of(c->page_size);
   p.slots_total = c->pages << p.page_shift;
   p.magnitude = w->magnitude;
-  return qg::launch_cache_write(p, tokens, c->head_dim, c->format == QG_W8A8_INT8, (cudaStream_t)stream, st.pdl) ==
+  return qg::launch_cache_write(p, c->head_dim, c->format == QG_W8A8_INT8, (cudaStream_t)stream, st.pdl) ==
                  cudaSuccess
              ? QG_OK
              : QG_ERR_CUDA;

@@ -26,85 +26,147 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
+// A lane's part in the rotation of its 8 channels: for halves the cosines and
+// signed sines of the 8, with the partner's values a shuffle away; for pairs
+// those of its 4 pairs.
+struct Turn {
+  uint64_t c[4], s[4];
+  int from;    // lane of the partner (halves)
+  bool on;
+};
+__device__ __forceinline__ void rotate(Chunk& x, const uint4& raw, const Turn& r, bool interleaved) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  if (interleaved) {
+    if (r.on) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // (a, b) (c, c) + (b, a) (-s, s)
+        const uint64_t swapped = pack_f32x2(__uint_as_float(w[j] & 0xffff0000u), __uint_as_float(w[j] << 16));
+        x[j] = fma_f32x2(swapped, r.s[j], mul_f32x2(x[j], r.c[j]));
+      }
+    }
+  } else {
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, w[0], r.from);
+    o.y = __shfl_sync(0xffffffffu, w[1], r.from);
+    o.z = __shfl_sync(0xffffffffu, w[2], r.from);
+    o.w = __shfl_sync(0xffffffffu, w[3], r.from);
+    if (r.on) {
+      Chunk y;
+      unpack_chunk(o, y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = fma_f32x2(y[j], r.s[j], mul_f32x2(x[j], r.c[j]));
+    }
+  }
+}
+
+// One token per blockIdx.x; its query, key and value rows are dealt to the
+// CTA's groups of L lanes, AHEAD passes of loads at a time: the first are in
+// flight while the turns are formed (8191 tokens of 32 + 2 x 8 heads: 39 us;
+// a pass at a time 43 us, several tokens per CTA 48 to 61 us).
 template <int D, bool INT8>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteParams p) {
   constexpr int L = D / 8;            // lanes per row
   constexpr int ROWS = kThreads / L;  // rows per pass of the CTA
-  __shared__ float2 turn[D / 2];      // (cos, sin) * magnitude
+  constexpr int AHEAD = 3;
+  __shared__ __align__(16) float turn_c[D / 2], turn_s[D / 2];
   griddep_launch_dependents();
   griddep_wait();
   const int t = blockIdx.x;
   const int half = p.rope_dim / 2;
-  if ((int)threadIdx.x < half) {
-    // whole turns drop out exactly: r = rint(x) and x - r are exact in 64 bits
-    const double x = (double)__ldg(p.positions + t) * (__ldg(p.frequency + threadIdx.x) * 0.15915494309189535);
-    float s, c;
-    sincospif(2.f * (float)(x - rint(x)), &s, &c);
-    turn[threadIdx.x] = make_float2(c * p.magnitude, s * p.magnitude);
-  }
-  __syncthreads();
-  const int lane = threadIdx.x % L;
+  const int lane = threadIdx.x % L, g = threadIdx.x / L;
+  const int rows = p.q_heads + 2 * p.kv_heads, step = gridDim.y * ROWS;
+  const uint4* qs = reinterpret_cast<const uint4*>(p.q + (size_t)t * p.ldq) + lane;
+  const uint4* ks = reinterpret_cast<const uint4*>(p.k + (size_t)t * p.ldk) + lane;
+  const uint4* vs = reinterpret_cast<const uint4*>(p.v + (size_t)t * p.ldv) + lane;
+  auto load = [&](int r) {
+    if (r < p.q_heads) return qs[r * L];
+    if (r < p.q_heads + p.kv_heads) return ks[(r - p.q_heads) * L];
+    if (r < rows) return vs[(r - p.q_heads - p.kv_heads) * L];
+    return make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 raw[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) raw[i] = load(blockIdx.y * ROWS + i * step + g);
   const int slot = __ldg(p.slots + t);
-  const bool store = slot >= 0 && slot < p.slots_total;
-  const int rows = p.q_heads + 2 * p.kv_heads;
-  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += gridDim.y * ROWS) {
-    const int r = r0 + threadIdx.x / L;
-    const bool live = r < rows;
-    const bool is_q = r < p.q_heads, is_k = !is_q && r < p.q_heads + p.kv_heads;
-    const int h = is_q ? r : (is_k ? r - p.q_heads : r - p.q_heads - p.kv_heads);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) {
-      const __nv_bfloat16* src = is_q   ? p.q + (size_t)t * p.ldq
-                                 : is_k ? p.k + (size_t)t * p.ldk
-                                        : p.v + (size_t)t * p.ldv;
-      unpack8(reinterpret_cast<const uint4*>(src + h * D)[lane], x);
+  Turn turn = {};
+  turn.on = lane * 8 < p.rope_dim;
+  turn.from = threadIdx.x & 31;
+  if (half > 0) {
+    if ((int)threadIdx.x < half) {
+      // whole turns drop out exactly: r = rint(x) and x - r are exact in 64 bits
+      const double x = (double)__ldg(p.positions + t) * (__ldg(p.frequency + threadIdx.x) * 0.15915494309189535);
+      float s, c;
+      sincospif(2.f * (float)(x - rint(x)), &s, &c);
+      turn_c[threadIdx.x] = c * p.magnitude;
+      turn_s[threadIdx.x] = s * p.magnitude;
     }
-    if (half > 0) {
-      const bool rot = (is_q || is_k) && lane * 8 < p.rope_dim;
-      if (p.interleaved) {
-        if (rot) {
+    __syncthreads();
+    // a lane's channels are the same in every row: its turn stays in registers
+    if (turn.on && p.interleaved) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 cs = turn[lane * 4 + j];
-            const float a = x[2 * j], b = x[2 * j + 1];
-            x[2 * j] = a * cs.x - b * cs.y;
-            x[2 * j + 1] = b * cs.x + a * cs.y;
-          }
-        }
-      } else {
-        // the partner of channel j is R/2 channels away: R/16 lanes (R % 16 == 0)
-        const int step = p.rope_dim / 16;
-        const bool low = lane < step;
-        const int partner = rot ? (low ? lane + step : lane - step) : lane;
-        const int from = (threadIdx.x & 31) - lane + partner;
+      for (int j = 0; j < 4; ++j) {
+        const float c = turn_c[lane * 4 + j], s = turn_s[lane * 4 + j];
+        turn.c[j] = pack_f32x2(c, c);
+        turn.s[j] = pack_f32x2(-s, s);
+      }
+    } else if (turn.on) {
+      // the partner of channel j is R/2 channels away: R/16 lanes (R % 16 == 0)
+      const int apart = p.rope_dim / 16;
+      const bool low = lane < apart;
+      const int at = (low ? lane : lane - apart) * 8;
+      turn.from += low ? apart : -apart;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float other = __shfl_sync(0xffffffffu, x[j], from);
-          if (rot) {
-            const float2 cs = turn[(low ? lane : lane - step) * 8 + j];
-            x[j] = low ? x[j] * cs.x - other * cs.y : x[j] * cs.x + other * cs.y;
-          }
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float2 c = *reinterpret_cast<const float2*>(turn_c + at + 2 * j);
+        const float2 s = *reinterpret_cast<const float2*>(turn_s + at + 2 * j);
+        turn.c[j] = pack_f32x2(c.x, c.y);
+        turn.s[j] = low ? pack_f32x2(-s.x, -s.y) : pack_f32x2(s.x, s.y);
       }
     }
-    Chunk y;
+  }
+  const bool store = slot >= 0 && slot < p.slots_total;
+  const size_t row0 = store ? ((size_t)(slot >> p.page_shift) * p.kv_heads << p.page_shift) +
+                                  (slot & ((1 << p.page_shift) - 1))
+                            : 0;
+  uint4* dst = reinterpret_cast<uint4*>(p.q_out + (size_t)t * p.ldqo) + lane;
+  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += AHEAD * step) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = pack_f32x2(x[2 * j], x[2 * j + 1]);
-    float a = absmax_chunk(y);
+    for (int i = 0; i < AHEAD; ++i) {
+      const int first = r0 + i * step;  // of the CTA's rows in this pass
+      const int r = first + g;
+      if (first >= rows) break;
+      const bool is_q = r < p.q_heads, is_k = !is_q && r < p.q_heads + p.kv_heads;
+      Chunk x;
+      unpack_chunk(raw[i], x);
+      if (half > 0 && first < p.q_heads + p.kv_heads) {
+        Turn own = turn;
+        own.on = turn.on && (is_q || is_k);
+        rotate(x, raw[i], own, p.interleaved);
+      }
+      if (first + ROWS <= p.q_heads) {  // queries only: rotated, rounded once
+        dst[r * L] = pack_chunk(x);
+        continue;
+      }
+      float a = absmax_chunk(x);
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) a = absmax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if (!live) continue;
-    if (is_q) {
-      reinterpret_cast<uint4*>(p.q_out + (size_t)t * p.ldqo + h * D)[lane] = pack_chunk(y);
-    } else if (store) {
-      const size_t row = ((size_t)(slot >> p.page_shift) * p.kv_heads + h << p.page_shift) +
-                         (slot & ((1 << p.page_shift) - 1));
-      float s, inv;
-      row_scale<INT8>(a, s, inv);
-      if (lane == 0) (is_k ? p.k_scale : p.v_scale)[row] = s;
-      reinterpret_cast<uint2*>((is_k ? p.k_codes : p.v_codes) + row * D)[lane] = chunk_codes<INT8>(y, s, inv);
+      for (int o = L / 2; o > 0; o >>= 1) a = absmax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+      if (is_q) {
+        dst[r * L] = pack_chunk(x);
+      } else if (r < rows && store) {
+        const int h = r - p.q_heads - (is_k ? 0 : p.kv_heads);
+        const size_t row = row0 + ((size_t)h << p.page_shift);
+        float s, inv;
+        row_scale<INT8>(a, s, inv);
+        if (lane == 0) (is_k ? p.k_scale : p.v_scale)[row] = s;
+        reinterpret_cast<uint2*>((is_k ? p.k_codes : p.v_codes) + row * D)[lane] = chunk_codes<INT8>(x, s, inv);
+      }
+    }
+    if (r0 + AHEAD * step < rows) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) raw[i] = load(r0 + (AHEAD + i) * step + g);
     }
   }
 }
@@ -183,16 +245,15 @@ cudaError_t launch(void (*fn)(P), const P& p, dim3 grid, cudaStream_t st, bool p
 
 }  // namespace
 
-cudaError_t launch_cache_write(const CacheWriteParams& p, int tokens, int head_dim, bool int8, cudaStream_t st,
+cudaError_t launch_cache_write(const CacheWriteParams& p, int head_dim, bool int8, cudaStream_t st,
                                bool pdl) {
   const int rows = p.q_heads + 2 * p.kv_heads;
   const int per = kThreads / (head_dim / 8);
   // few tokens: a CTA per pass of its rows, so that no pass waits for another
-  const int parts = tokens <= 2 * 148 ? (rows + per - 1) / per : 1;
-  const dim3 grid(tokens, parts);
+  const int parts = p.tokens <= 2 * 148 ? (rows + per - 1) / per : 1;
   auto fn = head_dim == 128 ? (int8 ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)
                             : (int8 ? cache_write_kernel<64, true> : cache_write_kernel<64, false>);
-  return launch(fn, p, grid, st, pdl);
+  return launch(fn, p, dim3(p.tokens, parts), st, pdl);
 }
 
 cudaError_t launch_cache_read(const CacheReadParams& p, int head_dim, bool int8, cudaStream_t st, bool pdl) {

@@ -82,11 +82,10 @@ struct CacheWriteParams {
   float *k_scale, *v_scale;
   const int *slots, *positions;
   const double* frequency;
-  int ldq, ldk, ldv, ldqo, q_heads, kv_heads, rope_dim, interleaved, page_shift, slots_total;
+  int tokens, ldq, ldk, ldv, ldqo, q_heads, kv_heads, rope_dim, interleaved, page_shift, slots_total;
   float magnitude;
 };
-cudaError_t launch_cache_write(const CacheWriteParams& p, int tokens, int head_dim, bool int8, cudaStream_t st,
-                               bool pdl);
+cudaError_t launch_cache_write(const CacheWriteParams& p, int head_dim, bool int8, cudaStream_t st, bool pdl);
 struct CacheReadParams {
   const uint8_t *k_codes, *v_codes;
   const float *k_scale, *v_scale;
