@@ -47,10 +47,8 @@ __device__ __forceinline__ float absmax_chunk(const Chunk& x) {
   return absmax_nan(absmax_nan(m[0], m[1]), absmax_nan(m[2], m[3]));
 }
 
-// Scale of a row, and its reciprocal.  Codes are x * (1 / scale) rounded, not
-// x / scale: the product is within 2^-22.9 of the quotient, so a code differs
-// only where the quotient is that near to a border between two codes, and the
-// division was a third of the norm's instructions (16384 x 5120: see norm.cu).
+// Scale of a row, and its reciprocal: correctly rounded, or 0 where it would
+// overflow (a scale below the normal range).
 template <bool INT8>
 __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
   amax = fabsf(amax);
@@ -59,33 +57,51 @@ __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
     inv = 0.f;
   } else {
     s = scale_of_amax<INT8>(amax);
-    // s = 0 only below 448 times the least fp32 number: such a row's codes are 0
-    inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-    if (inv > 3.402823466e38f) inv = 0.f;
+    inv = s >= 1.17549435e-38f ? __fdiv_rn(1.f, s) : 0.f;
   }
 }
 
-// Codes of 8 values, low byte first; all zero for a row whose scale is NaN.
+// Codes of 8 values, low byte first: round(x / s), as quant8 gives them; all
+// zero for a row whose scale is NaN.
+// The quotient is q = x inv, improved by its own remainder: with inv the
+// correctly rounded 1 / s and r = x - q s exact (fma), q + r inv is x / s to
+// 2^-46 before its one rounding, so the code is that of the divided quotient
+// (the plain product is not: it leaves the tie on one side or the other, and
+// bf16 values over amax / 127 are ties often).  Three two-wide instructions
+// for two values, where the division takes some twenty.
 template <bool INT8>
 __device__ __forceinline__ uint2 chunk_codes(const Chunk& x, float s, float inv) {
   if (s != s) return make_uint2(0u, 0u);
-  const uint64_t k = pack_f32x2(inv, inv);
+  float v[8];
+  if (inv != 0.f) {
+    const uint64_t k = pack_f32x2(inv, inv), ns = pack_f32x2(-s, -s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t q = mul_f32x2(x[j], k);
+      unpack_f32x2(fma_f32x2(fma_f32x2(q, ns, x[j]), k, q), v[2 * j], v[2 * j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      unpack_f32x2(x[j], v[2 * j], v[2 * j + 1]);
+      v[2 * j] = __fdiv_rn(v[2 * j], s);
+      v[2 * j + 1] = __fdiv_rn(v[2 * j + 1], s);
+    }
+  }
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float a, b, c, d;
-    unpack_f32x2(mul_f32x2(x[2 * h], k), a, b);
-    unpack_f32x2(mul_f32x2(x[2 * h + 1], k), c, d);
     if constexpr (INT8) {
-      // |x| inv <= 127 (1 + 2^-22): nothing to clamp but the pack's own range
-      const int q[4] = {__float2int_rn(a), __float2int_rn(b), __float2int_rn(c), __float2int_rn(d)};
+      // |x / s| <= 127 and a rounding: nothing to clamp but the pack's own range
+      const int q[4] = {__float2int_rn(v[4 * h]), __float2int_rn(v[4 * h + 1]), __float2int_rn(v[4 * h + 2]),
+                        __float2int_rn(v[4 * h + 3])};
       uint32_t r;
       asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\tcvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
           : "=r"(r)
           : "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]));
       w[h] = r;
     } else {
-      w[h] = cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
+      w[h] = cvt_e4m3x2(v[4 * h], v[4 * h + 1]) | (cvt_e4m3x2(v[4 * h + 2], v[4 * h + 3]) << 16);
     }
   }
   return make_uint2(w[0], w[1]);

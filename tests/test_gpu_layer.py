@@ -295,6 +295,26 @@ def test_cache_write(fmt, T, Hq, Hkv, D, rope, pairs, page):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_unrotated_rows_are_the_quantisers(fmt, D):
+    """Values, and keys without a rotation, get the codes and scales of quantize_act bit for bit: rows of
+    bf16 values with exact ties, ordinary rows, rows over the whole range of fp32 scales."""
+    g = _gen(D)
+    x = _rand(g, 4096, D)
+    x[:1024] = (torch.randint(-254, 255, (1024, D), generator=g, device="cuda") / 2).to(torch.bfloat16)  # k / 2
+    x[:1024, 0] = 127.0
+    x[1024:2048] = (x[1024:2048].float() * 2.0 ** torch.randint(-130, 120, (1024, 1), generator=g, device="cuda")).to(
+        torch.bfloat16)
+    op = qg.quantize_act(fmt, x)
+    cache = qg.Cache(fmt, 4096 // 64, 64, 1, D)
+    qg.cache_write(cache, x.view(-1, 1, D), x.view(-1, 1, D), torch.arange(4096, dtype=torch.int32, device="cuda"))
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        assert torch.equal(scale.view(-1), op.scale.view(torch.float32))
+        same = codes.view(-1, D) == op.q.view(-1, D)
+        assert same.all(), (int((~same).sum()), (~same).nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_cache_write_edge_rows(fmt):
     """Zero rows (scale 1), rows with a NaN or an infinity (scale NaN, codes 0, NaN when read)."""
     cache = qg.Cache(fmt, 2, 16, 1, 64)
