@@ -50,10 +50,10 @@ qg_status check_attend(const qg_cache* c, const qg_attend* a) {
   if (a->tree_mask && (!aligned(a->tree_mask, 8) || a->mask_words <= 0)) return QG_ERR_INVALID_ARG;
   if (!(a->scale > -3.0e38f && a->scale < 3.0e38f)) return QG_ERR_INVALID_ARG;
   if (a->batch > qg::kAttendMaxBatch || a->max_q > QGEMM_ATTEND_MAX_Q) return QG_ERR_UNSUPPORTED;
-  // positions of a sequence and units of work (at least 64 positions of 16
+  // positions of a sequence and units of work (at least 64 positions of 8
   // rows of one key head) are 32-bit
   const double positions = (double)a->max_pages * c->page_size;
-  const double tiles = (double)a->max_q * (a->q_heads / c->kv_heads) / 16 + 1;
+  const double tiles = (double)a->max_q * (a->q_heads / c->kv_heads) / 8 + 1;
   if (positions > 0x7fffff00 || (positions / 64 + 1) * tiles * c->kv_heads * a->batch > 0x7fffff00)
     return QG_ERR_UNSUPPORTED;
   return QG_OK;
@@ -268,7 +268,7 @@ qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, s
   p.err = st.err;
   p.wait_ns = st.wait_ns;
   CUtensorMap tk, tv;
-  if (!qg::attend_tiles(a->max_q * group)) {
+  if (!qg::attend_tiles(a->max_q * group, c->head_dim)) {
     const uint64_t rows = (uint64_t)c->pages * c->kv_heads * c->page_size;
     if (!qg::make_row_tmap(&tk, c->k, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;
     if (!qg::make_row_tmap(&tv, c->v, c->head_dim, rows, p.box_rows)) return QG_ERR_CUDA;

@@ -598,8 +598,15 @@ cudaError_t launch_rows_nr(const AttendParams& p, const CUtensorMap& tk, const C
 template <int D, bool INT8>
 cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int tile_rows, int ctas,
                         cudaStream_t st, bool pdl) {
-  return tile_rows == 8 ? launch_rows_nr<D, INT8, 1>(p, tk, tv, ctas, st, pdl)
-                        : launch_rows_nr<D, INT8, 2>(p, tk, tv, ctas, st, pdl);
+  switch (tile_rows) {
+    case 8: return launch_rows_nr<D, INT8, 1>(p, tk, tv, ctas, st, pdl);
+    case 16: return launch_rows_nr<D, INT8, 2>(p, tk, tv, ctas, st, pdl);
+    case 24: return launch_rows_nr<D, INT8, 3>(p, tk, tv, ctas, st, pdl);
+  }
+  if constexpr (D == 64) {
+    if (tile_rows == 32) return launch_rows_nr<D, INT8, 4>(p, tk, tv, ctas, st, pdl);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <int D, bool INT8>
@@ -627,21 +634,27 @@ cudaError_t launch_merge(const AttendParams& p, int tile_rows, int ctas, cudaStr
   return launch_pdl((const void*)qg_attend_merge_kernel<D, 2, 4>, dim3(ctas, tile_rows / 2), 256, 0, args, st, pdl);
 }
 
-// Rows of an item: the rows kernel takes 8 or 16 and reads the codes once per
-// item, so more rows go to the tile kernel, which reads them once per 128.
-int tile_rows_of(int rows_max) { return rows_max <= 8 ? 8 : rows_max <= 16 ? 16 : kTileRows; }
+// Rows of an item.  The rows kernel takes 8 to 24 (32 where a head of 64
+// leaves the registers) and its time per position grows with them; the tile
+// kernel's is that of 128 for any number.  16 sequences of up to 8000
+// positions, 8 key heads of 128: 24 rows 72 us against 88, 32 rows 95 (two
+// items of 16, or one that spills) against 90.
+int tile_rows_of(int rows_max, int head_dim) {
+  const int rows = rows_max <= 8 ? 8 : (rows_max + 7) / 8 * 8;
+  return rows <= (head_dim == 64 ? 32 : 24) ? rows : kTileRows;
+}
 
 }  // namespace
 
-bool attend_tiles(int rows_max) { return tile_rows_of(rows_max) == kTileRows; }
+bool attend_tiles(int rows_max, int head_dim) { return tile_rows_of(rows_max, head_dim) == kTileRows; }
 
 size_t attend_workspace(int head_dim, int rows_max, int sms) {
-  return sizeof(MergeRecord) * sms + (size_t)2 * sms * tile_rows_of(rows_max) * (head_dim + 2) * 4;
+  return sizeof(MergeRecord) * sms + (size_t)2 * sms * tile_rows_of(rows_max, head_dim) * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
                           const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl) {
-  const int rows = tile_rows_of(p.max_q * p.group);
+  const int rows = tile_rows_of(p.max_q * p.group, head_dim);
   p.records = static_cast<MergeRecord*>(workspace);
   p.partial = reinterpret_cast<float*>(p.records + sms);
   cudaError_t e;

@@ -14,10 +14,9 @@
 //         weights over the scores in TMEM.
 //   16-23 decode: codes from global memory to f16 in the swizzled operand
 //         tiles, the next tile's codes in registers meanwhile
-//   24    MMA: one thread issues S of tile j + 1 before O of tile j
+//   24    MMA: one thread issues scores and products as they can go
 //   25-27 the tiles ahead, in turn: where their positions lie, what of them
-//         counts, their scales (log2 and reciprocal once per position), and
-//         the prefetch of their codes into L2
+//         counts, and their scales (log2 and reciprocal once per position)
 //
 // What bounds it: per tile the two MMAs are 1024 tensor cycles, the 16384
 // exponentials 1024 cycles of the 16-wide unit, and shared memory carries 160
@@ -578,42 +577,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       // --------------------------------------------------------------- MMA --
       if (lane == 0) {
         const uint64_t qd = sdesc_sw128(q_tile), kd = sdesc_sw128(k_tile), vd = sdesc_mn_sw128(v_tile, kTilePos * 128);
-        int pieces = 0;              // whose scores have begun
-        int index = 0, next = 0;     // of tile j and j + 1 in their pieces
-        // turn j: scores of tile j + 1, then the product of tile j
-#pragma unroll 1
-        for (int j = -1; j < tiles && ok; ++j) {
-          index = next;
-          const int before = pieces - 1;  // pieces before tile j's
-          if (j + 1 < tiles) {
-            const int n = j + 1, st = n % kTileStages, s = n & 1;
-            if (!wait(&d_full[st], (n / kTileStages) & 1)) break;
-            next = descs[st].index;
-            mbar_arrive(&d_free[st]);
-            if (next == 0 && !wait(&q_full, pieces++ & 1)) break;
-            if (!wait(&k_full[s], (n >> 1) & 1)) break;
-            if (n >= 2 && !wait(&o_done[s], ((n - 2) >> 1) & 1)) break;  // the weights in these columns
-            tc_fence_after();
-            const uint64_t kt = kd + ((s * S::kOperand) >> 4);
+        // Scores and products each in tile order, whichever can go first: the
+        // scores of tile n wait for the product of n - 2 (its weights are in
+        // their columns), which other work can cover.
+        int pieces = 0, opened = 0;  // whose scores, whose products have begun
+        int n = 0, j = 0;            // next tile for scores, for the product
+        int n_index = -1;            // of tile n in its piece, -1: not looked up
+        uint32_t index = 0;          // bits 2 s, 2 s + 1: min(index, 2) of the tile in score columns s
+        unsigned long long since = 0;
+        int idle_turns = 0;
+        while (j < tiles) {
+          bool moved = false;
+          if (j < n) {
+            const int s = j & 1, at = (index >> (2 * s)) & 3;
+            if (mbar_test_wait(&w_full[s], (j >> 1) & 1) && mbar_test_wait(&v_full[s], (j >> 1) & 1) &&
+                // a piece's first product: the last piece is out
+                (at != 0 || opened == 0 || mbar_test_wait(&o_free, (opened - 1) & 1))) {
+              if (at == 0) ++opened;
+              tc_fence_after();
+              const uint64_t vt = vd + ((s * S::kOperand) >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t at = ((k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4;
-              mma_f16_ss(tmem + kTmemS + s * 128, qd + at, kt + at, idesc_f16(kTilePos, false), k > 0);
+              for (int k = 0; k < kTilePos / 16; ++k)
+                mma_f16_ts(tmem + kTmemO + s * 128, tmem + kTmemS + s * 128 + 8 * k, vt + ((k * 2048) >> 4),
+                           idesc_f16(D, true), at > 1 || k > 0);
+              mma_commit(&o_done[s]);
+              ++j;
+              moved = true;
             }
-            mma_commit(&s_full[s]);
           }
-          if (j >= 0) {
-            const int s = j & 1;
-            if (!wait(&w_full[s], (j >> 1) & 1) || !wait(&v_full[s], (j >> 1) & 1)) break;
-            // a piece's first product of either group: the last piece is out
-            if (index == 0 && before > 0 && !wait(&o_free, (before - 1) & 1)) break;
-            tc_fence_after();
-            const uint64_t vt = vd + ((s * S::kOperand) >> 4);
+          if (n < tiles && n < j + 2) {
+            const int s = n & 1, st = n % kTileStages;
+            if (n_index < 0 && mbar_test_wait(&d_full[st], (n / kTileStages) & 1)) {
+              n_index = descs[st].index;
+              mbar_arrive(&d_free[st]);
+            }
+            if (n_index >= 0 && mbar_test_wait(&k_full[s], (n >> 1) & 1) &&
+                (n < 2 || mbar_test_wait(&o_done[s], ((n - 2) >> 1) & 1)) &&
+                (n_index > 0 || mbar_test_wait(&q_full, pieces & 1))) {
+              if (n_index == 0) ++pieces;
+              tc_fence_after();
+              const uint64_t kt = kd + ((s * S::kOperand) >> 4);
 #pragma unroll
-            for (int k = 0; k < kTilePos / 16; ++k)
-              mma_f16_ts(tmem + kTmemO + s * 128, tmem + kTmemS + s * 128 + 8 * k, vt + ((k * 2048) >> 4),
-                         idesc_f16(D, true), index > 1 || k > 0);
-            mma_commit(&o_done[s]);
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = ((k >> 2) * (kTilePos * 128) + (k & 3) * 32) >> 4;
+                mma_f16_ss(tmem + kTmemS + s * 128, qd + at, kt + at, idesc_f16(kTilePos, false), k > 0);
+              }
+              mma_commit(&s_full[s]);
+              index = (index & ~(3u << (2 * s))) | ((uint32_t)min(n_index, 2) << (2 * s));
+              n_index = -1;
+              ++n;
+              moved = true;
+            }
+          }
+          if (moved) {
+            idle_turns = 0;
+          } else if ((++idle_turns & 63) == 0) {
+            // bounded, like every wait
+            const unsigned long long now = globaltimer();
+            if (idle_turns == 64) since = now;
+            else if (now - since > p.wait_ns) {
+              atomicOr(p.err, kErrWaitTimeout);
+              break;
+            }
           }
         }
         // MMAs still in flight (a wait ran out) end before TMEM is given up
@@ -647,10 +672,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
           row = (page * p.kv_heads + x.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
           ks = __ldg(reinterpret_cast<const float4*>(p.k_scale + row));
           vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + row));
-          if ((lane & 3) == 0) {
-            bulk_prefetch_l2(k_codes + (size_t)row * D, 16 * D);
-            bulk_prefetch_l2(v_codes + (size_t)row * D, 16 * D);
-          }
         }
         const int st = j % kTileStages;
         if (j >= kTileStages) wait(&d_free[st], (j / kTileStages - 1) & 1);

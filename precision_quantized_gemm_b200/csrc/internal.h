@@ -114,7 +114,7 @@ struct AttendParams {
 };
 constexpr int kAttendMaxBatch = 1024;
 size_t attend_workspace(int head_dim, int rows_max, int sms);
-bool attend_tiles(int rows_max);  // whether the tile kernel takes so many rows per key head
+bool attend_tiles(int rows_max, int head_dim);  // whether the tile kernel takes so many rows per key head
 cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
                           const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl);
 
