@@ -36,6 +36,7 @@
 // and accumulator keep the same reference, so the result is unchanged.
 #pragma once
 #include "attend_common.cuh"
+#include "f32x2.cuh"
 
 namespace qg {
 

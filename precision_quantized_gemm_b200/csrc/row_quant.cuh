@@ -4,6 +4,7 @@
 // are 0, so that it reads back as NaN and its codes stay finite (a cached row
 // that a mask hides must not reach a sum: 0 * code is 0, 0 * NaN is not).
 #pragma once
+#include "f32x2.cuh"
 #include "ptx.cuh"
 #include "quant_math.cuh"
 
