@@ -446,7 +446,7 @@ qg_status qgemm_norm(const qg_norm* n, int M, int N, qg_format f, qg_operand* ou
  *     k_scale, v_scale: fp32  [pages, kv_heads, page_size]
  * so that a page's rows of one head are contiguous.  head_dim 64 or 128,
  * page_size a power of two from 16 to 1024 (QG_ERR_UNSUPPORTED otherwise, and
- * for pages * kv_heads * page_size >= 2^31). */
+ * for pages * kv_heads * page_size or kv_heads * head_dim >= 2^31). */
 typedef struct {
   qg_format format;
   int32_t pages, page_size, kv_heads, head_dim;
@@ -503,9 +503,9 @@ qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, 
  * positions a token sees, with key head h / (q_heads / kv_heads):
  *     out = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
  * A token that sees nothing gets zeros and lse -inf.  Rows of out and lse that
- * belong to no sequence are left as they were.  What a token does not see
- * does not reach it, NaN rows included; a NaN row that it sees, key or value,
- * makes its out and lse NaN.
+ * belong to no sequence are left as they were; out and lse overlap none of the
+ * inputs.  What a token does not see does not reach it, NaN rows included; a
+ * NaN row that it sees, key or value, makes its out and lse NaN.
  * Device values are taken within bounds: offsets to [0, tokens], kv_len to
  * [0, max_pages * page_size], pages to [0, pages); drafted tokens past max_q
  * get no output.  batch <= 1024, max_q <= QGEMM_ATTEND_MAX_Q

@@ -26,6 +26,8 @@ qg_status check_cache(const qg_cache* c) {
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return QG_ERR_INVALID_ARG;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
     return QG_ERR_INVALID_ARG;
+  // a token's row of heads is counted in 32 bits, like the strides
+  if ((long long)c->kv_heads * c->head_dim > 0x7fffffffLL) return QG_ERR_UNSUPPORTED;
   return QG_OK;
 }
 int shift_of(int pow2) {

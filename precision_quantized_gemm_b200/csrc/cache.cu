@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "internal.h"
@@ -250,7 +251,8 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, int head_dim, bool int
   const int rows = p.q_heads + 2 * p.kv_heads;
   const int per = kThreads / (head_dim / 8);
   // few tokens: a CTA per pass of its rows, so that no pass waits for another
-  const int parts = p.tokens <= 2 * 148 ? (rows + per - 1) / per : 1;
+  // (up to the grid's limit; further passes are a CTA's next)
+  const int parts = p.tokens <= 2 * 148 ? std::min((rows + per - 1) / per, 65535) : 1;
   auto fn = head_dim == 128 ? (int8 ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)
                             : (int8 ? cache_write_kernel<64, true> : cache_write_kernel<64, false>);
   return launch(fn, p, dim3(p.tokens, parts), st, pdl);

@@ -294,6 +294,23 @@ def test_cache_write(fmt, T, Hq, Hkv, D, rope, pairs, page):
     assert all(torch.equal(a, b) for a, b in zip(before, (cache.k, cache.v, cache.k_scale)))
 
 
+def test_cache_write_of_very_many_heads():
+    """More passes of rows than a grid has places for: the first, the last and those in between."""
+    Hq, D = 8 * 65535 + 1000, 128
+    g = _gen(0)
+    q, k = _rand(g, 1, Hq, D), _rand(g, 1, 1, D)
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rope = qg.Rope(qg.rope_frequencies(D)[0])
+    cache = qg.Cache(qg.QG_FP8_DYNAMIC, 1, 16, 1, D)
+    out = qg.cache_write(cache, k, k, one, q=q, rope=rope, positions=one + 7)
+    first = cache.k.clone(), cache.v.clone()
+    cut = Hq // 2
+    for part, want in ((q[:, :cut], out[:, :cut]), (q[:, cut:], out[:, cut:])):
+        got = qg.cache_write(cache, k, k, one, q=part, rope=rope, positions=one + 7)
+        assert torch.equal(got, want)
+    assert torch.equal(first[0], cache.k) and torch.equal(first[1], cache.v)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("D", [64, 128])
 def test_unrotated_rows_are_the_quantisers(fmt, D):
@@ -465,6 +482,40 @@ def test_single_tokens(fmt, lens, ns, Hq, Hkv, D, page):
 def test_trees(fmt, tree, lens, ns, Hq, Hkv, D, page):
     b = Batch(fmt, lens, ns, Hq, Hkv, D, page, seed=sum(ns) + Hq, tree=tree)
     b.check(*b.run(), rows=6)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens,ns,Hq,Hkv,D,page", [  # rows of a key head: 20, 24, 24, 28, 32, 32
+    ([500, 40, 1000], [1, 1, 1], 20, 1, 128, 64), ([900, 77], [3, 2], 16, 2, 128, 16), ([130, 700], [2, 3], 8, 1, 64, 32),
+    ([700, 90], [7, 5], 8, 2, 64, 128), ([1200, 100], [4, 8], 8, 2, 64, 16), ([1200, 100], [4, 8], 8, 2, 128, 16)])
+def test_row_counts_between(fmt, lens, ns, Hq, Hkv, D, page):
+    """The most rows that the warp-level kernel takes, and the first that go to the tiles."""
+    b = Batch(fmt, lens, ns, Hq, Hkv, D, page, seed=sum(lens) + D, tree=ns[0] > 1)
+    b.check(*b.run(), rows=6)
+
+
+@pytest.mark.parametrize("Hq,n", [(20, 1), (64, 9)])
+def test_one_workspace_in_two_graphs(Hq, n):
+    """Two captured calls of different sizes share a workspace and are replayed in turn on one stream."""
+    b = Batch(qg.QG_FP8_DYNAMIC, [900, 1200], [n, n], Hq, 4, 128, 16, seed=2)
+    c = Batch(qg.QG_W8A8_INT8, [3000], [1], 8, 2, 64, 64, seed=3, tree=False)
+    want = [x.run() for x in (b, c)]
+    ws, graphs, got = qg.Workspace("cuda"), [], []
+    for x in (b, c):
+        x.run(workspace=ws)  # the workspace is as large as the larger needs
+    torch.cuda.synchronize()
+    for x in (b, c):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(x.run(workspace=ws))
+        graphs.append(graph)
+    for turn in (0, 1, 1, 0, 1):
+        for t in got[turn]:
+            t.fill_(7)
+        graphs[turn].replay()
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
 
 
 @pytest.mark.parametrize("fmt", FMTS)

@@ -112,6 +112,14 @@ def test_cache_is_checked(change):
     assert qg.qgemm_attend(c, _attend(), P, 1 << 30, None) == INVALID
 
 
+def test_a_token_of_too_many_channels():
+    """kv_heads * head_dim past 32 bits: no stride could hold it."""
+    c = _cache(pages=1, kv_heads=1 << 25, head_dim=128)
+    assert qg.qgemm_cache_write(c, _write(), 3, None) == UNSUPPORTED
+    assert qg.qgemm_cache_read(c, P, 3, P, 128, P, 128, None) == UNSUPPORTED
+    assert qg.qgemm_attend(c, _attend(q_heads=1 << 25), P, 1 << 30, None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("change", [
     dict(slots=None), dict(slots=P + 2), dict(k=None), dict(ldk=120), dict(ldv=124), dict(q=None), dict(q_out=None),
     dict(q_heads=0), dict(q_heads=-1), dict(ldq=248), dict(ldqo=128), dict(rope_dim=72), dict(rope_dim=8),
