@@ -507,8 +507,9 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
 
 // Merge of the items that span CTAs: CTA c takes the one of its record, ROWS
 // rows per blockIdx.y.  WPR warps share a row: each takes every WPR-th part,
-// D / 32 channels a lane; they meet in shared memory.
-template <int D, int ROWS, int WPR>
+// D / 32 channels a lane; they meet in shared memory.  TILE: parts as the tile
+// kernel's fragments lie.
+template <int D, int ROWS, int WPR, bool TILE>
 __global__ void __launch_bounds__(ROWS * WPR * 32) qg_attend_merge_kernel(const AttendParams p, int tile_rows) {
   constexpr int CPL = D / 32;
   __shared__ float acc_s[ROWS][WPR][D], sum_s[ROWS][WPR];
@@ -532,8 +533,20 @@ __global__ void __launch_bounds__(ROWS * WPR * 32) qg_attend_merge_kernel(const 
     const float* part = part_of(c);
     const float m = part[tile_rows * D + row], l = part[tile_rows * D + tile_rows + row];
     float v[CPL];
-    if constexpr (CPL == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
-    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(part + row * D + lane * 2);
+    if constexpr (TILE) {
+      // fragments of 16 rows x 8 channels: lane 4 g + t of its warp left
+      // channels 2 t, 2 t + 1 of rows g and g + 8
+      const int c = lane * CPL;
+      const float* at = part + (((row >> 4) * (D / 8) + (c >> 3)) * 32 + (row & 7) * 4 + ((c & 7) >> 1)) * 4 +
+                        ((row >> 3) & 1) * 2;
+#pragma unroll
+      for (int j = 0; j < CPL; j += 2)
+        *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(at + j * 2);
+    } else if constexpr (CPL == 4) {
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+    } else {
+      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(part + row * D + lane * 2);
+    }
     const float f = m == kNegInf ? 0.f : ex2(m - top);
     sum = fmaf(l, f, sum);
 #pragma unroll
@@ -630,8 +643,8 @@ template <int D>
 cudaError_t launch_merge(const AttendParams& p, int tile_rows, int ctas, cudaStream_t st, bool pdl) {
   void* args[] = {(void*)&p, (void*)&tile_rows};
   if (tile_rows == kTileRows)
-    return launch_pdl((const void*)qg_attend_merge_kernel<D, 16, 1>, dim3(ctas, kTileRows / 16), 512, 0, args, st, pdl);
-  return launch_pdl((const void*)qg_attend_merge_kernel<D, 2, 4>, dim3(ctas, tile_rows / 2), 256, 0, args, st, pdl);
+    return launch_pdl((const void*)qg_attend_merge_kernel<D, 16, 1, true>, dim3(ctas, kTileRows / 16), 512, 0, args, st, pdl);
+  return launch_pdl((const void*)qg_attend_merge_kernel<D, 2, 4, false>, dim3(ctas, tile_rows / 2), 256, 0, args, st, pdl);
 }
 
 // Rows of an item.  The rows kernel takes 8 to 24 (32 where a head of 64

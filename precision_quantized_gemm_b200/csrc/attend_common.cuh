@@ -120,9 +120,10 @@ __device__ __forceinline__ Share plan_units(const AttendParams& p, int tile_rows
   }
   if (l == 31) s.warp_tot[w] = inc;
   __syncthreads();
-  int run = inc - sum;
-#pragma unroll 1
-  for (int j = 0; j < w; ++j) run += s.warp_tot[j];
+  int run = l < w ? s.warp_tot[l] : 0;  // of the warps before
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) run += __shfl_xor_sync(0xffffffffu, run, d);
+  run += inc - sum;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     run += s.pre[b + 1];

@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
   // rows (two turns each)
   __shared__ __align__(8) uint64_t l_full[2][2][8];
   __shared__ float l_turn[2][2][kTileRows], m_turn[2][2][kTileRows];
+  __shared__ uint32_t seen[16][16][4];  // a softmax warp's rows: which of a tile's positions they see
+  __shared__ float q_down[16][16];      // and the inverse of their queries' power
   __shared__ uint32_t tmem_ptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
@@ -217,36 +219,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       if (opens) {
         // its queries, f16, each row's largest magnitude brought to
         // [2^14, 2^15).  The group of the piece's first tile stores them; the
-        // other needs the powers alone.  Here lanes l and l + 16 share row
-        // rw + l, half of the channels each.
+        // other needs the powers alone.  Lane l knows row rw + l % 16's place;
+        // the lanes of a load share rows of D / 8 chunks.
         item = x.item;
         live = x.row0 + rw < x.rows;
-        const int row = rw + (lane & 15), r = x.row0 + row;
+        const int r = x.row0 + rw + (lane & 15);
         const int mine = r < x.rows ? r / p.group : -1;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (size_t)(x.tok0 + max(mine, 0)) * p.ldq + (x.head * p.group + (mine < 0 ? 0 : r - mine * p.group)) * D +
-            (lane >> 4) * (D / 2));
-        float amax = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 v = mine >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const long long place =
+            (long long)(x.tok0 + max(mine, 0)) * p.ldq + (x.head * p.group + (mine < 0 ? 0 : r - mine * p.group)) * D;
+        // the last piece's scores are done with its queries
+        if (x.index == 0 && j > 0) wait(&s_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
+        const bool store = x.index == 0 && __all_sync(0xffffffffu, ok);
+        constexpr int LR = D / 8, RPL = 32 / LR;
+        const int chunk = lane % LR;
+#pragma unroll 1
+        for (int b = lane / LR; b < 16; b += 4 * RPL) {
+          uint4 v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
-        float up, down;
-        row_power(amax, up, down);
-        if (x.index == 0) {
-          // the last piece's scores are done with the queries
-          if (j > 0) wait(&s_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
-          if (__all_sync(0xffffffffu, ok)) {
-            const uint32_t dst = q_tile + row * 128 + (D == 128 ? (uint32_t)(lane >> 4) * (kTileRows * 128) : 0u);
-#pragma unroll 2
-            for (int c = 0; c < D / 16; ++c) {
-              const uint4 v = mine >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < 4; ++i) {
+            const long long at = __shfl_sync(0xffffffffu, place, b + i * RPL);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (__shfl_sync(0xffffffffu, mine, b + i * RPL) >= 0)
+              v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + at) + chunk);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            // bf16 magnitudes are ordered like their bits, two to a word
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+#pragma unroll
+            for (int d = LR / 2; d > 0; d >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
+            float up, down;
+            row_power(__uint_as_float(max(top << 16, top & 0xffff0000u)), up, down);
+            if (chunk == 0) q_down[warp][b + i * RPL] = down;
+            if (store) {
               uint32_t f[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -254,31 +262,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
                     __floats2half2_rn(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
                 f[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
-              const int chunk = D == 128 ? c : (lane >> 4) * (D / 16) + c;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((chunk ^ (row & 7)) << 4)), "r"(f[0]),
-                           "r"(f[1]), "r"(f[2]), "r"(f[3])
+              const int row = rw + b + i * RPL;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               q_tile + (chunk >> 3) * (kTileRows * 128) + row * 128 + (((chunk ^ row) & 7) << 4)),
+                           "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
                            : "memory");
             }
-            fence_proxy_async_smem();
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_full);
         }
+        if (x.index == 0) fence_proxy_async_smem();
+        __syncwarp();
+        if (x.index == 0 && lane == 0) mbar_arrive(&q_full);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          power[i] = __shfl_sync(0xffffffffu, down, 8 * i + g) * p.scale_log2;
+          power[i] = q_down[warp][8 * i + g] * p.scale_log2;
           tok[i] = __shfl_sync(0xffffffffu, mine, 8 * i + g);
           m[i] = kNegInf;
           l2[i] = 0;
         }
       }
       const uint32_t sc = scales + st * S::kScales + t * 8;
+      const bool part_seen = x.before < kTilePos || x.count < kTilePos;
+      if (part_seen && live) {
+        // while the scores are on their way
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          seen[warp][8 * i + g][t] = (uint32_t)seen_bits(p, x.tok0, tok[i], x.count - t * 32, x.before - t * 32);
+        __syncwarp();
+      }
       // the scores of this tile followed this group's last product (the MMA
       // thread waits for it): the accumulator may be read and scaled
       wait(&s_full[group], (j >> 1) & 1);
       if (live && __all_sync(0xffffffffu, ok)) {
         tc_fence_after();
-        const bool part_seen = x.before < kTilePos || x.count < kTilePos;
         // 32 positions at a time
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -300,8 +316,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
           if (part_seen) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t bits =
-                  (uint32_t)(seen_bits(p, x.tok0, tok[i], x.count - c * 32, x.before - c * 32) >> (2 * t));
+              const uint32_t bits = seen[warp][8 * i + g][c] >> (2 * t);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -451,7 +466,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
               const int row = rw + 8 * i + g, r = x.row0 + row;
               const size_t tk = x.tok0 + max(tok[i], 0);
               const int h = tok[i] < 0 ? 0 : x.head * p.group + r - tok[i] * p.group;
-              at[i] = whole ? tk * p.ldo + h * D + 2 * t : (size_t)row * D + 2 * t;
+              at[i] = tk * p.ldo + h * D + 2 * t;
               if (t == 0 && tok[i] >= 0) {
                 if (!whole) {
                   part[kTileRows * D + row] = m[i];
@@ -467,28 +482,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
                 of[i] *= inv;
               }
             }
-            const uint32_t other = tmem + ((uint32_t)rw << 16) + kTmemO + (group ^ 1) * 128;
+            // (alone, its own again with a factor of 0)
+            const uint32_t other = both ? tmem + ((uint32_t)rw << 16) + kTmemO + (group ^ 1) * 128 : o_at;
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t o[8], q[8];
               tmem_ld_16x256b(o_at + c, o);
-              if (both) tmem_ld_16x256b(other + c, q);
+              tmem_ld_16x256b(other + c, q);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (tok[i] >= 0) {
+              for (int k = 0; k < 2; ++k) {
+                float y[4];
 #pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    float a = __uint_as_float(o[4 * k + 2 * i]) * f[i], b = __uint_as_float(o[4 * k + 2 * i + 1]) * f[i];
-                    if (both) {
-                      a = fmaf(__uint_as_float(q[4 * k + 2 * i]), of[i], a);
-                      b = fmaf(__uint_as_float(q[4 * k + 2 * i + 1]), of[i], b);
-                    }
-                    if (whole)
-                      *reinterpret_cast<__nv_bfloat162*>(p.out + at[i] + c + 8 * k) = __floats2bfloat162_rn(a, b);
-                    else
-                      *reinterpret_cast<float2*>(part + at[i] + c + 8 * k) = make_float2(a, b);
-                  }
+                for (int e = 0; e < 4; ++e)
+                  y[e] = fmaf(__uint_as_float(q[4 * k + e]), of[e >> 1], __uint_as_float(o[4 * k + e]) * f[e >> 1]);
+                if (!*static_cast<const volatile int*>(&x.whole)) {
+                  // as the fragments lie: whole lines (the merge knows)
+                  reinterpret_cast<float4*>(part)[((rw >> 4) * (D / 8) + c / 8 + k) * 32 + lane] =
+                      make_float4(y[0], y[1], y[2], y[3]);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (tok[i] >= 0)
+                      *reinterpret_cast<__nv_bfloat162*>(p.out + at[i] + c + 8 * k) =
+                          __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
                 }
               }
               __syncwarp();
@@ -652,8 +669,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       // Warp 25 + i takes tiles i, i + 3, ...: the chain from page table to
       // scales is longer than a tile's turn.  Lane i has positions 4 i .. 4 i
       // + 3: within one run of 16, whose row its first lane hands on.
-      if (warp == 25 && lane == 0) p.records[blockIdx.x] = merge_record(p, sched, share, kTileRows);
-      __syncwarp();
       Piece x = {};
       int item = 0, done = 0;  // units of the item at hand: [item, done)
 #pragma unroll 1
@@ -709,6 +724,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_full[st]);
       }
+      if (warp == 25 && lane == 0) p.records[blockIdx.x] = merge_record(p, sched, share, kTileRows);
     }
   }
   tc_fence_before();
