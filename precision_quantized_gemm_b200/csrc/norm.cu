@@ -93,19 +93,28 @@ __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, b
   unpack_f32x2(q, a, c);
   const float r = rsqrtf(cta_sum(a + c, red + 36) * inv_n + eps);
   const uint64_t r2 = pack_f32x2(r, r), o2 = pack_f32x2(offset, offset);
+  // what a call may leave out is asked for once, around the chunks: asked for
+  // in each, it is issued all the same, with its lanes off
+  auto scaled = [&](bool with_offset) {
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int at = threadIdx.x + i * blockDim.x;
-    if (FULL || at < nch) {
-      Chunk v;
-      unpack_chunk(__ldg(w + at), v);
-      if (offset != 0.f) {
+    for (int i = 0; i < CH; ++i) {
+      const int at = threadIdx.x + i * blockDim.x;
+      if (FULL || at < nch) {
+        Chunk v;
+        unpack_chunk(__ldg(w + at), v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = add_f32x2(v[j], o2);
+        for (int j = 0; j < 4; ++j) x[i][j] = mul_f32x2(mul_f32x2(x[i][j], r2), with_offset ? add_f32x2(v[j], o2) : v[j]);
       }
+    }
+  };
+  if (offset != 0.f) scaled(true);
+  else scaled(false);
+  if (b != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = mul_f32x2(mul_f32x2(x[i][j], r2), v[j]);
-      if (b != nullptr) {
+    for (int i = 0; i < CH; ++i) {
+      const int at = threadIdx.x + i * blockDim.x;
+      if (FULL || at < nch) {
+        Chunk v;
         unpack_chunk(__ldg(b + at), v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[i][j] = add_f32x2(x[i][j], v[j]);
@@ -151,20 +160,31 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512, CH == 4 ? 2 : 1) norm_ke
     norm_row<CH, FULL>(v, nch, p.inv_n, p.post_norm == QG_NORM_LAYER, p.eps, p.post_weight, p.post_bias, p.weight_offset,
                  red);
   const uint64_t bs = pack_f32x2(p.block_scale, p.block_scale), rs = pack_f32x2(p.residual_scale, p.residual_scale);
+  if (gr != nullptr) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (FULL || c < nch) {
+        Chunk gv;
+        unpack_chunk(gr[c], gv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = mul_f32x2(v[i][j], gv[j]);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (gr != nullptr && (FULL || c < nch)) {
-      Chunk gv;
-      unpack_chunk(gr[c], gv);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = mul_f32x2(v[i][j], gv[j]);
-    }
     Chunk r;
     unpack_chunk(rv[i], r);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[i][j] = fma_f32x2(rs, r[j], mul_f32x2(bs, v[i][j]));
-    if (p.h != nullptr && (FULL || c < nch)) reinterpret_cast<uint4*>(p.h + (size_t)m * p.ldh)[c] = pack_chunk(v[i]);
+  }
+  if (p.h != nullptr) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (FULL || c < nch) reinterpret_cast<uint4*>(p.h + (size_t)m * p.ldh)[c] = pack_chunk(v[i]);
+    }
   }
   if (!p.pre_norm) return;
   norm_row<CH, FULL>(v, nch, p.inv_n, p.pre_norm == QG_NORM_LAYER, p.eps, p.pre_weight, p.pre_bias, p.weight_offset,

@@ -156,10 +156,11 @@ def norm(residual, weight, x=None, *, bias=None, kind="rms", post_weight=None, p
             return norm(residual, weight, x, bias=bias, kind=kind, post_weight=post_weight, post_bias=post_bias,
                         gate=gate, block_scale=block_scale, residual_scale=residual_scale, eps=eps,
                         weight_offset=weight_offset, fmt=fmt, out=out, h=h, y=y, static_amax=static_amax)
+    # (new_empty takes half the time of torch.empty; the inputs' types are checked below)
     if h is None and (x is not None or weight is None):
-        h = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        h = first.new_empty((M, N))
     if weight is not None and fmt is None and y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        y = first.new_empty((M, N))
     if fmt is not None and out is None:
         out = _operand(fmt, M, N, dev)
     a = qg_norm(residual_scale=residual_scale, block_scale=block_scale, eps=eps, weight_offset=weight_offset)
@@ -318,7 +319,7 @@ def cache_write(cache: Cache, k, v, slots, q=None, rope: Rope | None = None, pos
             raise ValueError("q: bf16 [tokens, q_heads, head_dim] wanted")
         Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+            q_out = q.new_empty((T, Hq, D))
         a.q_heads, a.ldq, a.ldqo = Hq, _heads("q", q, T, Hq, D, dev), _heads("q_out", q_out, T, Hq, D, dev)
         a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -341,7 +342,7 @@ def cache_read(cache: Cache, slots, k=None, v=None, stream=None):
             return cache_read(cache, slots, k=k, v=v)
     shape = (T, cache.kv_heads, cache.head_dim)
     k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    v = k.new_empty(shape) if v is None else v
     check(lib().qgemm_cache_read(cache.c, _ints("slots", slots, (T,), dev), T, k.data_ptr(),
                                  _heads("k", k, *shape, dev), v.data_ptr(), _heads("v", v, *shape, dev), _here(dev)),
           "qgemm_cache_read")
@@ -371,7 +372,7 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
         with _there(dev, stream):
             return attend(cache, q, q_offsets, kv_len, page_table, tree_mask=tree_mask, scale=scale, max_q=max_q,
                           out=out, lse=lse, workspace=workspace)
-    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
+    out = q.new_empty((T, Hq, D)) if out is None else out
     a = qg_attend(ldq=_heads("q", q, T, Hq, cache.head_dim, dev), ldo=_heads("out", out, T, Hq, D, dev),
                   q=q.data_ptr(), out=out.data_ptr(), q_offsets=_ints("q_offsets", q_offsets, (B + 1,), dev),
                   kv_len=_ints("kv_len", kv_len, (B,), dev), page_table=_ints("page_table", page_table, (B, pages), dev),
