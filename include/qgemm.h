@@ -439,8 +439,9 @@ qg_status qgemm_norm(const qg_norm* n, int M, int N, qg_format f, qg_operand* ou
                      void* stream);
 
 /* A paged cache of keys and values, quantised per (token, head) row with the
- * row formats: QG_FP8_DYNAMIC (e4m3, scale amax / 448) or QG_W8A8_INT8 (int8,
- * scale amax / 127).  Place o of page g is slot g * page_size + o; its row of
+ * row formats: QG_FP8_DYNAMIC (e4m3, scale amax * (1 / 448)) or QG_W8A8_INT8
+ * (int8, scale amax * (1 / 127)); reciprocal and product are fp32, a code is
+ * the fp32 quotient by the scale, rounded.  Place o of page g is slot g * page_size + o; its row of
  * head h is row (g * kv_heads + h) * page_size + o of
  *     k, v:             codes [pages, kv_heads, page_size, head_dim]
  *     k_scale, v_scale: fp32  [pages, kv_heads, page_size]

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
         const int h = r - p.q_heads - (is_k ? 0 : p.kv_heads);
         const size_t row = row0 + ((size_t)h << p.page_shift);
         float s, inv;
-        row_scale<INT8>(a, s, inv);
+        row_scale<INT8, true>(a, s, inv);
         if (lane == 0) (is_k ? p.k_scale : p.v_scale)[row] = s;
         reinterpret_cast<uint2*>((is_k ? p.k_codes : p.v_codes) + row * D)[lane] = chunk_codes<INT8>(x, s, inv);
       }

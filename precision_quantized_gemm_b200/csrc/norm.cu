@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512, CH == 4 ? 2 : 1) norm_ke
     a = cta_absmax(a, red + 144);
     const bool int8 = p.format == QG_W8A8_INT8;
     float s, inv;
-    if (int8) row_scale<true>(a, s, inv);
-    else row_scale<false>(a, s, inv);
+    if (int8) row_scale<true, false>(a, s, inv);
+    else row_scale<false, false>(a, s, inv);
     if (threadIdx.x == 0) static_cast<float*>(p.scale)[m] = s;
     uint2* q = reinterpret_cast<uint2*>(p.q + (size_t)m * p.N);
 #pragma unroll
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512, CH == 4 ? 2 : 1) norm_ke
       for (int o = 8; o > 0; o >>= 1) a = absmax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
       if ((FULL || c < nch)) {
         float s, inv;
-        row_scale<false>(a, s, inv);
+        row_scale<false, false>(a, s, inv);
         if ((c & 15) == 0) static_cast<float*>(p.scale)[(size_t)m * (p.N / 128) + c / 16] = s;
         q[c] = chunk_codes<false>(v[i], s, inv);
       }

@@ -49,15 +49,21 @@ __device__ __forceinline__ float absmax_chunk(const Chunk& x) {
 }
 
 // Scale of a row, and its reciprocal: correctly rounded, or 0 where it would
-// overflow (a scale below the normal range).
-template <bool INT8>
+// overflow (a scale below the normal range).  An operand's scale is the
+// quantisers' divided one.  A cached row's (CACHED) is the product with the
+// rounded 1 / 448 or 1 / 127, which is how a division by a constant is
+// computed for tensors: the two differ by a unit in the last place at most,
+// but bf16 values lie on the ties of the codes often (1 in 16 where amax is
+// 1.75 times a power of two), and a tie goes the way its scale leans.
+template <bool INT8, bool CACHED>
 __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
   amax = fabsf(amax);
   if (!(amax <= 3.402823466e38f)) {
     s = __uint_as_float(0x7fc00000u);
     inv = 0.f;
   } else {
-    s = scale_of_amax<INT8>(amax);
+    if constexpr (CACHED) s = amax > 0.f ? __fmul_rn(amax, 1.f / (INT8 ? 127.f : 448.f)) : 1.f;
+    else s = scale_of_amax<INT8>(amax);
     inv = s >= 1.17549435e-38f ? __fdiv_rn(1.f, s) : 0.f;
   }
 }

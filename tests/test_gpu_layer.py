@@ -313,22 +313,42 @@ def test_cache_write_of_very_many_heads():
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("D", [64, 128])
-def test_unrotated_rows_are_the_quantisers(fmt, D):
-    """Values, and keys without a rotation, get the codes and scales of quantize_act bit for bit: rows of
-    bf16 values with exact ties, ordinary rows, rows over the whole range of fp32 scales."""
+def test_unrotated_rows_bit_for_bit(fmt, D):
+    """Values, and keys without a rotation: the scale is the fp32 product amax * (1 / top), the codes are those of
+    the correctly rounded quotient (formed in 64 bits: 53 >= 2 * 24 + 2 bits round once more like the division).
+    Rows of bf16 values with exact ties, ordinary rows, rows over the whole range of fp32 scales."""
     g = _gen(D)
     x = _rand(g, 4096, D)
     x[:1024] = (torch.randint(-254, 255, (1024, D), generator=g, device="cuda") / 2).to(torch.bfloat16)  # k / 2
     x[:1024, 0] = 127.0
+    x[512:1024, 0] = 224.0
     x[1024:2048] = (x[1024:2048].float() * 2.0 ** torch.randint(-130, 120, (1024, 1), generator=g, device="cuda")).to(
         torch.bfloat16)
-    op = qg.quantize_act(fmt, x)
+    one = torch.ones((), device="cuda")
+    amax = x.float().abs().amax(-1)
+    want_scale = torch.where(amax > 0, amax * (one / _top(fmt)), one)
+    quotient = (x.double() / want_scale.double()[:, None]).float()
+    want = quotient.round().to(torch.int8) if fmt == qg.QG_W8A8_INT8 else quotient.to(torch.float8_e4m3fn)
     cache = qg.Cache(fmt, 4096 // 64, 64, 1, D)
     qg.cache_write(cache, x.view(-1, 1, D), x.view(-1, 1, D), torch.arange(4096, dtype=torch.int32, device="cuda"))
     for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
-        assert torch.equal(scale.view(-1), op.scale.view(torch.float32))
-        same = codes.view(-1, D) == op.q.view(-1, D)
+        assert torch.equal(scale.view(-1), want_scale)
+        same = codes.view(-1, D) == want.view(torch.uint8)
         assert same.all(), (int((~same).sum()), (~same).nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("fmt", [qg.QG_FP8_DYNAMIC, qg.QG_W8A8_INT8])
+def test_norm_codes_are_the_quantisers(fmt):
+    """y in bf16 values (weights and rows chosen so that y is exact in bf16): the operand is quantize_act's, bit for bit."""
+    g = _gen(3)
+    N = 512
+    x = (torch.randint(0, 2, (300, N), generator=g, device="cuda") * 2 - 1).to(torch.bfloat16)  # mean square 1
+    w = (torch.randint(-254, 255, (N,), generator=g, device="cuda") / 2).to(torch.bfloat16)
+    w[0] = 127.0
+    r = qg.norm(x, w, fmt=fmt, eps=0.0)
+    op = qg.quantize_act(fmt, x * w)
+    assert torch.equal(r.operand.q.view(-1), op.q.view(-1)) and torch.equal(
+        r.operand.scale.view(torch.float32), op.scale.view(torch.float32))
 
 
 @pytest.mark.parametrize("fmt", FMTS)
