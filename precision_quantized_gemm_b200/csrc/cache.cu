@@ -11,7 +11,10 @@
 //
 // Bound: HBM for many tokens, latency for few.  A row of head_dim elements is
 // head_dim / 8 neighbouring lanes of 8 elements, so amax is a shuffle; cos and
-// sin of a token are computed once per CTA and shared.
+// sin of a token are computed once per CTA and shared.  8191 tokens of 32 + 2 x
+// 8 heads of 128: written in 40 us (4.6 TB/s, 71 % of a copy's rate; the warps
+// wait for loads half of the time, and the issue slots are 64 % full).  100,000
+// tokens of 8 heads read in 107 us (5.8 TB/s, 89 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,7 +68,7 @@ __device__ __forceinline__ void rotate(Chunk& x, const uint4& raw, const Turn& r
 
 // One token per blockIdx.x; its query, key and value rows are dealt to the
 // CTA's groups of L lanes, AHEAD passes of loads at a time: the first are in
-// flight while the turns are formed (8191 tokens of 32 + 2 x 8 heads: 39 us;
+// flight while the turns are formed (8191 tokens of 32 + 2 x 8 heads: 40 us;
 // a pass at a time 43 us, several tokens per CTA 48 to 61 us).
 template <int D, bool INT8>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteParams p) {
@@ -251,7 +254,8 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, int head_dim, bool int
   const int rows = p.q_heads + 2 * p.kv_heads;
   const int per = kThreads / (head_dim / 8);
   // few tokens: a CTA per pass of its rows, so that no pass waits for another
-  // (up to the grid's limit; further passes are a CTA's next)
+  // (up to the grid's limit; further passes are a CTA's next).  32 tokens of 40
+  // + 2 x 8 heads: 4.2 us, 6.2 with a CTA per token; 600 tokens: 10.4 us, 6.2.
   const int parts = p.tokens <= 2 * 148 ? std::min((rows + per - 1) / per, 65535) : 1;
   auto fn = head_dim == 128 ? (int8 ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)
                             : (int8 ? cache_write_kernel<64, true> : cache_write_kernel<64, false>);

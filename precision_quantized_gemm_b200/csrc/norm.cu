@@ -10,7 +10,11 @@
 //
 // Bound: HBM for many rows (each input read once, each output written once),
 // latency for few.  One CTA owns a row, which stays in registers (chunks of 8
-// elements per thread) between its up to five reductions.
+// elements per thread) between its up to five reductions.  16384 x 5120 with a
+// post norm, to e4m3: 107 us, 5.5 TB/s (84 % of a copy's rate; as bf16 without
+// the post norm 103 us, all of it); the issue slots are 66 % full (29
+// instructions an element), so instructions are what else there is to save.
+// 1 x 5120: 4.1 us in a graph, launch included.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -124,7 +128,7 @@ __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, b
 }
 
 template <int CH, bool FULL>
-__global__ void __launch_bounds__(CH == 1 ? 1024 : 512, CH == 4 ? 2 : 1) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(512, CH == 4 ? 2 : 1) norm_kernel(const NormParams p) {
   __shared__ __align__(16) float red[5 * 36];
   griddep_launch_dependents();
   griddep_wait();
@@ -284,9 +288,13 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t st, bool pdl) {
   // NVFP4 also writes the scale rows that pad the last 128-row atom
   const int rows = p.q != nullptr && p.format == QG_NVFP4 ? (p.M + 127) / 128 * 128 : p.M;
   auto threads = [&](int ch) { return ((nch + ch - 1) / ch + 31) / 32 * 32; };
-  // few rows: the shortest chain, a chunk a thread
-  if (threads(1) <= 1024 && p.M <= 2 * 148) return launch_ch<1>(p, rows, threads(1), st, pdl);
-  if (threads(2) <= 128) return launch_ch<2>(p, rows, threads(2), st, pdl);
+  // Few rows, or narrow ones: two chunks a thread, the shorter chain (1 x 5120:
+  // 4.3 us, 6.2 with four; 296 x 8192: 6.5, 8.3; 2048 x 1024: 6.2, 8.3; one
+  // chunk is no shorter).  Many: four, which spread the reductions and scales
+  // over more elements (16384 x 5120: 107 us, 139 with two; 2048: 45, 52; at
+  // 16384 x 1024 both take 28 to 29).  Eight only where four would need more
+  // than 512 threads (16384 x 8192: 170 us with eight, 167 with four).
+  if (threads(2) <= (p.M <= 2 * 148 ? 512 : 64)) return launch_ch<2>(p, rows, threads(2), st, pdl);
   if (threads(4) <= 512) return launch_ch<4>(p, rows, threads(4), st, pdl);
   return launch_ch<8>(p, rows, threads(8), st, pdl);
 }
