@@ -257,6 +257,21 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
       const int st = (blk / WARPS) % kStages;
       const uint32_t kb = ring + st * S::kStage, vb = kb + S::kCodes, sb = scale_ring + st * S::kScale;
       const int pos0 = begin + blk * kBlock;
+      const bool tail = pos0 + kBlock > end || pos0 + kBlock > past;
+      uint32_t seen[NR][2];  // of the block's positions, from this lane's first on
+      if (tail) {
+        // while the block is on its way
+        unsigned long long drafted[NR][2];
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) drafted[i][e] = drafted_bits(p, tok0, tok[i][e], past - pos0);
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            seen[i][e] = (uint32_t)(seen_bits(p, tok[i][e], end - pos0, past - pos0, drafted[i][e]) >> g);
+      }
       if (ok) ok = mbar_wait(bar + st, (phase >> st) & 1, p.err, p.wait_ns);
       phase ^= 1u << st;
       ok = __all_sync(0xffffffffu, ok);
@@ -307,21 +322,18 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) sc[mt][h] = pos_scale[warp][mt * 16 + h * 8 + g];
-      const bool tail = pos0 + kBlock > end || pos0 + kBlock > past;
       bool grown = false;
 #pragma unroll
       for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          uint32_t see = 0xffffffffu;  // bits of the block's positions from this lane's first on
-          if (tail) see = (uint32_t)(seen_bits(p, tok0, tok[i][e], end - pos0, past - pos0) >> g);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& v = s[mt][i][2 * h + e];
               v = fmaf(v * power[i][e], sc[mt][h].x, sc[mt][h].y);
-              if (tail && !((see >> (mt * 16 + h * 8)) & 1)) v = kNegInf;
+              if (tail && !((seen[i][e] >> (mt * 16 + h * 8)) & 1)) v = kNegInf;
               grown |= v > m[i][e] + kRescaleAt;  // m = -inf: anything seen
             }
         }

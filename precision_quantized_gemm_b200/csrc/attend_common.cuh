@@ -194,25 +194,28 @@ __device__ __forceinline__ MergeRecord merge_record(const AttendParams& p, const
 // Which of 64 positions token i of a sequence sees, as bits: of the first
 // `count`, the `before` that precede the drafted tokens (negative: the first
 // is drafted token -before), and the drafted ones of its mask row.  (i < 0: a
-// row past the last, nothing.)
-__device__ __forceinline__ unsigned long long seen_bits(const AttendParams& p, int tok0, int i, int count,
-                                                        int before) {
+// row past the last, nothing.)  In two steps, so that the loads for several
+// rows are in flight together: the mask row's bits from the window on, and
+// what the window makes of them.
+__device__ __forceinline__ unsigned long long drafted_bits(const AttendParams& p, int tok0, int i, int before) {
+  if (p.mask == nullptr) return 0ull;  // causal: nothing to load
+  const int word = before < 0 ? -before >> 6 : 0, shift = before < 0 ? -before & 63 : 0;
+  const unsigned long long* row = p.mask + (size_t)(tok0 + max(i, 0)) * p.mask_words;
+  unsigned long long bits = 0, next = 0;
+  if (i >= 0 && word < p.mask_words) bits = __ldg(row + word);
+  if (i >= 0 && shift > 0 && word + 1 < p.mask_words) next = __ldg(row + word + 1);
+  return shift > 0 ? bits >> shift | next << (64 - shift) : bits;
+}
+__device__ __forceinline__ unsigned long long seen_bits(const AttendParams& p, int i, int count, int before,
+                                                        unsigned long long drafted) {
   if (i < 0 || count <= 0) return 0ull;
   const unsigned long long all = count >= 64 ? ~0ull : (1ull << count) - 1;
   if (before >= 64) return all;
-  unsigned long long drafted;  // bit e: drafted token e - before (a negative one is not cached)
   if (p.mask == nullptr) {
     const int n = i + 1 + before;  // drafted tokens up to i
     drafted = n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
-  } else {
-    const unsigned long long* row = p.mask + (size_t)(tok0 + i) * p.mask_words;
-    if (before >= 0) {
-      drafted = __ldg(row) << before;
-    } else {
-      const int word = -before >> 6, shift = -before & 63;
-      drafted = word < p.mask_words ? __ldg(row + word) >> shift : 0ull;
-      if (shift && word + 1 < p.mask_words) drafted |= __ldg(row + word + 1) << (64 - shift);
-    }
+  } else if (before > 0) {
+    drafted <<= before;
   }
   const unsigned long long prefix = before > 0 ? (1ull << before) - 1 : 0ull;
   return all & (prefix | drafted);

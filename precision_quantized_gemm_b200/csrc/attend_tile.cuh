@@ -285,9 +285,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
       const bool part_seen = x.before < kTilePos || x.count < kTilePos;
       if (part_seen && live) {
         // while the scores are on their way
+        unsigned long long drafted[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) drafted[i] = drafted_bits(p, x.tok0, tok[i], x.before - t * 32);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          seen[warp][8 * i + g][t] = (uint32_t)seen_bits(p, x.tok0, tok[i], x.count - t * 32, x.before - t * 32);
+          seen[warp][8 * i + g][t] = (uint32_t)seen_bits(p, tok[i], x.count - t * 32, x.before - t * 32, drafted[i]);
         __syncwarp();
       }
       // the scores of this tile followed this group's last product (the MMA
