@@ -45,13 +45,14 @@ template <int D, int NR>
 struct RowsSmem {
   static constexpr int kCodes = kBlock * D;                  // K or V codes of a stage
   static constexpr int kStage = 2 * kCodes;
-  static constexpr int kRing = kRowsWarps<NR> * kStages * kStage;
+  // a warp's results of a piece lie in its own ring, empty by then
+  static constexpr int kMergeRow = D + 4;                    // floats; spreads rows over banks
+  static constexpr int kResult = 8 * NR * kMergeRow * 4;
+  static constexpr int kWarpRing = kStages * kStage > kResult ? kStages * kStage : (kResult + 1023) / 1024 * 1024;
+  static constexpr int kRing = kRowsWarps<NR> * kWarpRing;
   static constexpr int kScale = 2 * kBlock * 4;              // K and V scales of a stage
   static constexpr int kScales = kRowsWarps<NR> * kStages * kScale;
   static constexpr int kTotal = 1024 + kRing + kScales;
-  // the warps' partial results meet in the ring, empty by then
-  static constexpr int kMergeRow = D + 4;                    // floats; spreads rows over banks
-  static_assert(4 * 8 * NR * kMergeRow * 4 <= kRing, "merge buffers fit the ring");
 };
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int row) {
@@ -123,9 +124,9 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t ring = base + warp * kStages * S::kStage;
+  const uint32_t ring = base + warp * S::kWarpRing;
   const uint32_t scale_ring = base + S::kRing + warp * kStages * S::kScale;
-  float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
+  const float* results = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)));
   uint64_t* bar = bars + warp * kStages;
   if (lane == 0)
     for (int i = 0; i < kStages; ++i) mbar_init(bar + i, 1);
@@ -143,9 +144,10 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
   uint32_t phase = 0;  // bit i: parity of the ring stage's next wait
   bool ok = true, drained = false;
 
+  Piece x = find_piece(p, sched, ROWS, share_begin, share_end);
 #pragma unroll 1
   for (int u = share_begin; u < share_end;) {
-    const Piece x = find_piece(p, sched, ROWS, u, share_end);
+    if (u > share_begin) next_piece(p, sched, ROWS, kUnit, u, share_end, x);
     const int tok0 = sched.tok0[x.seq], len = sched.len[x.seq];
     const int rows = min(sched.n[x.seq], p.max_q) * p.group;
     const int begin = x.unit0 * kUnit, end = min(x.unit1 * kUnit, len);
@@ -179,40 +181,53 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
         bulk_floats(sc + kBlock * 4, p.v_scale + row, p.box_rows * 4, bar + st);
       }
     };
-    // the ring is empty between items (a stage's parity carries on); reads and
-    // writes of the last item's blocks come before the copies that refill it
+    // What the piece needs from memory is asked for at once: its queries, the
+    // pages of the first blocks, then the blocks.
+    // query row g of each row tile
+    uint4 qv[NR][D / 64][2];
+    int mine[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int row = x.row0 + 8 * i + g;
+      mine[i] = row < rows ? row / p.group : -1;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (size_t)(tok0 + max(mine[i], 0)) * p.ldq +
+          (x.head * p.group + (mine[i] < 0 ? 0 : row - mine[i] * p.group)) * D);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)  // 16-channel chunks t (and t + 4)
+#pragma unroll
+        for (int hlf = 0; hlf < 2; ++hlf)
+          qv[i][c][hlf] = mine[i] >= 0 ? __ldg(src + (t + 4 * c) * 2 + hlf) : make_uint4(0, 0, 0, 0);
+    }
+    int first_page[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) first_page[i] = page_of(warp + i * WARPS);
+    int ahead = warp + kStages * WARPS;
+    int next_page = page_of(ahead);
+    // the ring is empty between pieces (a stage's parity carries on); reads and
+    // writes of the last piece's results come before the copies that refill it
     fence_proxy_async_smem();
     __syncwarp();
-    int ahead = warp;
-    int next_page = page_of(ahead);
     if (ok) {
-#pragma unroll 1
-      for (int i = 0; i < kStages; ++i) {
-        if (ahead < nblk) issue(ahead, next_page);
-        ahead += WARPS;
-        next_page = page_of(ahead);
-      }
+#pragma unroll
+      for (int i = 0; i < kStages; ++i)
+        if (warp + i * WARPS < nblk) issue(warp + i * WARPS, first_page[i]);
     }
 
-    // query row g of each row tile, f16, channels in the order of the key
-    // reads; scale and drafted token of rows 2 t and 2 t + 1, the lane's score
-    // columns (-1: past the last row)
+    // f16, channels in the order of the key reads; scale and drafted token of
+    // rows 2 t and 2 t + 1, the lane's score columns (-1: past the last row)
     uint32_t qb[NR][KS][2];
     float power[NR][2];
     int tok[NR][2];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int row = x.row0 + 8 * i + g;
-      const int mine = row < rows ? row / p.group : -1;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (size_t)(tok0 + max(mine, 0)) * p.ldq + (x.head * p.group + (mine < 0 ? 0 : row - mine * p.group)) * D);
       float amax = 0.f;
       uint32_t raw[KS][2];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)  // 16-channel chunks t (and t + 4)
+      for (int c = 0; c < D / 64; ++c)
 #pragma unroll
         for (int hlf = 0; hlf < 2; ++hlf) {
-          const uint4 v = mine >= 0 ? __ldg(src + (t + 4 * c) * 2 + hlf) : make_uint4(0, 0, 0, 0);
+          const uint4 v = qv[i][c][hlf];
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -235,7 +250,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         power[i][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4) * p.scale_log2;
-        tok[i][e] = __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
+        tok[i][e] = __shfl_sync(0xffffffffu, mine[i], (2 * t + e) * 4);
       }
     }
 
@@ -425,7 +440,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
       for (int i = 0; i < kStages; ++i) (void)mbar_wait(bar + i, (phase >> i) & 1, p.err, p.wait_ns);
     }
 
-    // the warps' partials meet: maxima, then the scaled sums 4 warps at a time
+    // the warps' results meet, each in its own ring with its own reference
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -437,41 +452,14 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
           part_m[warp][8 * i + 2 * t + e] = m[i][e];
           part_l[warp][8 * i + 2 * t + e] = l[i][e];
         }
+        const uint32_t dst = ring + ((8 * i + 2 * t + e) * S::kMergeRow + (D / 8) * g) * 4;
+#pragma unroll
+        for (int j = 0; j < MT; j += 2)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 8 * j), "f"(o[i][j][e]), "f"(o[i][j][2 + e]),
+                       "f"(o[i][j + 1][e]), "f"(o[i][j + 1][2 + e])
+                       : "memory");
       }
     __syncthreads();
-    float f[NR][2];
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = kNegInf;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, part_m[w][8 * i + 2 * t + e]);
-        f[i][e] = m[i][e] == kNegInf ? 0.f : ex2(m[i][e] - top);
-      }
-#pragma unroll 1
-    for (int turn = WARPS / 4 - 1; turn >= 0; --turn) {
-      if (warp / 4 == turn) {
-        float* dst = merge + (warp % 4) * ROWS * S::kMergeRow;
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int j = 0; j < MT; j += 2) {
-              float4* d4 =
-                  reinterpret_cast<float4*>(dst + (8 * i + 2 * t + e) * S::kMergeRow + (D / 8) * g + 2 * j);
-              float4 v = make_float4(o[i][j][e] * f[i][e], o[i][j][2 + e] * f[i][e], o[i][j + 1][e] * f[i][e],
-                                     o[i][j + 1][2 + e] * f[i][e]);
-              if (turn < WARPS / 4 - 1) {
-                const float4 a = *d4;
-                v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
-              }
-              *d4 = v;
-            }
-      }
-      __syncthreads();
-    }
     const bool whole = x.unit0 == 0 && x.unit1 == x.units;
     const int slot = 2 * blockIdx.x + (u == share_begin ? 0 : 1);
     float* part = p.partial + (size_t)slot * ROWS * (D + 2);
@@ -481,14 +469,14 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
       float top = kNegInf, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) top = fmaxf(top, part_m[w][row]);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w)
-        sum += part_m[w][row] == kNegInf ? 0.f : part_l[w][row] * ex2(part_m[w][row] - top);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(merge + (w * ROWS + row) * S::kMergeRow + c0);
-        acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = part_m[w][row] == kNegInf ? 0.f : ex2(part_m[w][row] - top);
+        const float4 v =
+            *reinterpret_cast<const float4*>(results + w * (S::kWarpRing / 4) + row * S::kMergeRow + c0);
+        sum = fmaf(part_l[w][row], f, sum);
+        acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
       }
       if (whole) {
         const int r = x.row0 + row;
@@ -511,7 +499,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
         }
       }
     }
-    fence_proxy_async_smem();  // the merge buffers become the ring again
+    fence_proxy_async_smem();  // the results' places become the ring again
     __syncthreads();
     u += x.unit1 - x.unit0;
   }

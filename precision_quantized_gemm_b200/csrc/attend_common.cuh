@@ -164,6 +164,25 @@ __device__ __forceinline__ Piece find_piece(const AttendParams& p, const Sched& 
   return x;
 }
 
+// The piece after x in a share: the next item from its first unit (u) on,
+// without a search or a division.  Call with u < end.
+__device__ __forceinline__ void next_piece(const AttendParams& p, const Sched& s, int tile_rows, int unit, int u, int end,
+                                           Piece& x) {
+  x.row0 += tile_rows;
+  if (x.row0 >= min(s.n[x.seq], p.max_q) * p.group) {
+    x.row0 = 0;
+    if (++x.head == p.kv_heads) {
+      x.head = 0;
+      // past sequences without tokens; u < end: there is one with units
+      do ++x.seq;
+      while (s.pre[x.seq + 1] <= u);
+      x.units = max((s.len[x.seq] + unit - 1) / unit, 1);
+    }
+  }
+  x.unit0 = 0;
+  x.unit1 = min(x.units, end - u);
+}
+
 // What the merge has to know of an item that starts in a CTA's share and goes
 // on past it (there is at most one): every CTA of the grid leaves one record
 // in the workspace, `last` < 0 for none.  The parts are this CTA's slot and
