@@ -36,6 +36,11 @@ int shift_of(int pow2) {
   return s;
 }
 
+// Rows per key head: what an attention's kernel and workspace go by.
+long long rows_per_key_head(const qg_cache* c, const qg_attend* a) {
+  return (long long)a->max_q * (a->q_heads / c->kv_heads);
+}
+
 qg_status check_attend(const qg_cache* c, const qg_attend* a) {
   if (!a) return QG_ERR_INVALID_ARG;
   const qg_status s = check_cache(c);
@@ -55,8 +60,8 @@ qg_status check_attend(const qg_cache* c, const qg_attend* a) {
   // positions of a sequence and units of work (at least 64 positions of 8
   // rows of one key head) are 32-bit
   const double positions = (double)a->max_pages * c->page_size;
-  const double tiles = (double)a->max_q * (a->q_heads / c->kv_heads) / 8 + 1;
-  if (positions > 0x7fffff00 || (positions / 64 + 1) * tiles * c->kv_heads * a->batch > 0x7fffff00)
+  const double tiles = (double)rows_per_key_head(c, a) / 8 + 1;
+  if (rows_per_key_head(c, a) > 0x7fff0000 || positions > 0x7fffff00 || (positions / 64 + 1) * tiles * c->kv_heads * a->batch > 0x7fffff00)
     return QG_ERR_UNSUPPORTED;
   return QG_OK;
 }
@@ -232,7 +237,8 @@ qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, 
 // -------------------------------------------------------------- attention --
 size_t qgemm_attend_workspace_size(const qg_cache* c, const qg_attend* a) {
   if (!c || !a || c->head_dim <= 0 || c->kv_heads <= 0 || a->q_heads <= 0 || a->max_q <= 0) return 0;
-  return qg::attend_workspace(c->head_dim, a->max_q * (a->q_heads / c->kv_heads), qg::device_sm_count());
+  const long long rows = rows_per_key_head(c, a);
+  return rows > 0x7fff0000 ? 0 : qg::attend_workspace(c->head_dim, (int)rows, qg::device_sm_count());
 }
 
 qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, size_t ws_bytes, void* stream) {

@@ -514,6 +514,37 @@ def test_row_counts_between(fmt, lens, ns, Hq, Hkv, D, page):
     b.check(*b.run(), rows=6)
 
 
+@pytest.mark.parametrize("B,Hq,most", [(1024, 4, 1), (700, 3, 3), (300, 64, 5)])
+def test_many_sequences(B, Hq, most):
+    """More sequences than threads plan, a third of them without tokens, some without positions."""
+    r = np.random.default_rng(B)
+    ns = [int(n) if i % 3 else 0 for i, n in enumerate(r.integers(1, most + 1, B))]
+    lens = [0 if i % 7 == 1 else int(a) for i, a in enumerate(r.integers(most, 150, B))]
+    b = Batch(qg.QG_FP8_DYNAMIC, lens, ns, Hq, 1, 64, 16, seed=B, tree=most > 1)
+    b.check(*b.run(), rows=1)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+@pytest.mark.parametrize("Hq,n", [(8, 2), (64, 9)])
+def test_any_scale(Hq, n, scale):
+    b = Batch(qg.QG_W8A8_INT8, [300, 90], [n, 1], Hq, 2, 128, 32, seed=5)
+    b.check(*b.run(scale=scale), scale=scale, rows=3)
+
+
+def test_offsets_that_start_late():
+    """Rows before the first sequence belong to none, and offsets past the tokens are cut."""
+    b = Batch(qg.QG_FP8_DYNAMIC, [200, 77], [2, 3], 8, 2, 128, 16, seed=5, tree=False)
+    want, want_lse = b.run()
+    q = b.q.clone()
+    b.q[4:] = q[:4]
+    b.offs += 4  # 4, 6, 9 of 8 rows
+    out, lse = torch.full_like(b.q, 7.0), torch.full((8, 8), 7.0, device="cuda")
+    qg.attend(b.cache, b.q, b.offs, b.lens_t, b.table, out=out, lse=lse, max_q=3)
+    assert (out[:4] == 7).all() and (lse[:4] == 7).all()
+    assert torch.equal(out[4:6], want[:2]) and torch.equal(lse[4:6], want_lse[:2])
+    assert (out[6:] != 7).any() and out[6:].isfinite().all()
+
+
 @pytest.mark.parametrize("Hq,n", [(20, 1), (64, 9)])
 def test_one_workspace_in_two_graphs(Hq, n):
     """Two captured calls of different sizes share a workspace and are replayed in turn on one stream."""

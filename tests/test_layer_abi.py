@@ -112,6 +112,13 @@ def test_cache_is_checked(change):
     assert qg.qgemm_attend(c, _attend(), P, 1 << 30, None) == INVALID
 
 
+def test_rows_per_key_head_past_32_bits():
+    """max_q * q_heads / kv_heads is counted in 32 bits."""
+    c, a = _cache(kv_heads=1), _attend(q_heads=1 << 24, max_q=256, batch=1, max_pages=1, ldq=1 << 30, ldo=1 << 30)
+    assert qg.qgemm_attend_workspace_size(c, a) == 0
+    assert qg.qgemm_attend(c, a, P, 1 << 30, None) == UNSUPPORTED
+
+
 def test_a_token_of_too_many_channels():
     """kv_heads * head_dim past 32 bits: no stride could hold it."""
     c = _cache(pages=1, kv_heads=1 << 25, head_dim=128)
