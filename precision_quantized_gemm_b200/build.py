@@ -29,7 +29,7 @@ SOURCES = ["api.cu", "quant.cu", "gemm_fp8.cu", "gemm_int8.cu", "gemm_block.cu",
            "api_layer.cu", "norm.cu", "cache.cu", "attend.cu"]
 HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "gemm_launch.cuh", "internal.h", "quant_math.cuh", "attr_cache.h", "skinny.cuh",
            "persist.cuh", "row_quant.cuh", "attend_common.cuh", "attend_tile.cuh",
-           "f32x2.cuh"]
+           "f32x2.cuh", "loads.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -6,8 +6,8 @@
 // query heads that share a key head are stacked (row = token * group + head).
 // With key codes kc and scale ks, value codes vc and scale vs:
 //   s_j = scale * log2(e) * (q . kc_j) ks_j            (base-2 scores)
-//   t_j = s_j + log2(vs_j),  m = max_j t_j
-//   w_j = 2^(t_j - m)  in [0, 1],   l = sum_j w_j / vs_j
+//   t_j = s_j + log2(vs_j),  m: max_j t_j, or less by up to kRescaleAt
+//   w_j = 2^(t_j - m)  in [0, 256],  l = sum_j w_j / vs_j
 //   o   = sum_j w_j vc_j / l,       lse = ln 2 (m + log2 l)
 // so the value scale rides in the exponent and the weights are f16 (11 bits;
 // bf16 would give them 8): a weight below 2^-24 of the largest adds nothing
@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "loads.cuh"
 #include "ptx.cuh"
 
 namespace qg {
@@ -98,10 +99,10 @@ __device__ __forceinline__ Share plan_units(const AttendParams& p, int tile_rows
   int sum = 0;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const int a = min(max(__ldg(p.q_offsets + b), 0), p.tokens);
-    const int n = max(min(max(__ldg(p.q_offsets + b + 1), 0), p.tokens) - a, 0);
+    const int a = min(max(fresh(p.q_offsets + b), 0), p.tokens);
+    const int n = max(min(max(fresh(p.q_offsets + b + 1), 0), p.tokens) - a, 0);
     // the table's row covers ldp pages
-    const int len = min(max(__ldg(p.kv_len + b), 0), p.ldp << p.page_shift);
+    const int len = min(max(fresh(p.kv_len + b), 0), p.ldp << p.page_shift);
     s.tok0[b] = a;
     s.n[b] = n;
     s.len[b] = len;
@@ -221,8 +222,8 @@ __device__ __forceinline__ unsigned long long drafted_bits(const AttendParams& p
   const int word = before < 0 ? -before >> 6 : 0, shift = before < 0 ? -before & 63 : 0;
   const unsigned long long* row = p.mask + (size_t)(tok0 + max(i, 0)) * p.mask_words;
   unsigned long long bits = 0, next = 0;
-  if (i >= 0 && word < p.mask_words) bits = __ldg(row + word);
-  if (i >= 0 && shift > 0 && word + 1 < p.mask_words) next = __ldg(row + word + 1);
+  if (i >= 0 && word < p.mask_words) bits = fresh(row + word);
+  if (i >= 0 && shift > 0 && word + 1 < p.mask_words) next = fresh(row + word + 1);
   return shift > 0 ? bits >> shift | next << (64 - shift) : bits;
 }
 __device__ __forceinline__ unsigned long long seen_bits(const AttendParams& p, int i, int count, int before,

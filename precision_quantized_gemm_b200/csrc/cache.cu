@@ -94,14 +94,14 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
   uint4 raw[AHEAD];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) raw[i] = load(blockIdx.y * ROWS + i * step + g);
-  const int slot = __ldg(p.slots + t);
+  const int slot = fresh(p.slots + t);
   Turn turn = {};
   turn.on = lane * 8 < p.rope_dim;
   turn.from = threadIdx.x & 31;
   if (half > 0) {
     if ((int)threadIdx.x < half) {
       // whole turns drop out exactly: r = rint(x) and x - r are exact in 64 bits
-      const double x = (double)__ldg(p.positions + t) * (__ldg(p.frequency + threadIdx.x) * 0.15915494309189535);
+      const double x = (double)fresh(p.positions + t) * (fresh(p.frequency + threadIdx.x) * 0.15915494309189535);
       float s, c;
       sincospif(2.f * (float)(x - rint(x)), &s, &c);
       turn_c[threadIdx.x] = c * p.magnitude;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
   for (long long r = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L; r < rows;
        r += (long long)gridDim.x * (kThreads / L)) {
     const int t = (int)(r / p.kv_heads), h = (int)(r % p.kv_heads);
-    const int slot = __ldg(p.slots + t);
+    const int slot = fresh(p.slots + t);
     uint4 k[2], v[2];
     if (slot >= 0 && slot < p.slots_total) {
       const size_t row = ((size_t)(slot >> p.page_shift) * p.kv_heads + h << p.page_shift) +

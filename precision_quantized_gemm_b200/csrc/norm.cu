@@ -69,7 +69,7 @@ __device__ __forceinline__ float cta_absmax(float v, float* red) {
 // FULL: every thread has all CH chunks.
 template <int CH, bool FULL>
 __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, bool layer, float eps,
-                                         const uint4* __restrict__ w, const uint4* __restrict__ b, float offset,
+                                         const uint4* w, const uint4* b, float offset,
                                          float* red) {
   if (layer) {
     uint64_t s = 0;
@@ -105,7 +105,7 @@ __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, b
       const int at = threadIdx.x + i * blockDim.x;
       if (FULL || at < nch) {
         Chunk v;
-        unpack_chunk(__ldg(w + at), v);
+        unpack_chunk(fresh(w + at), v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[i][j] = mul_f32x2(mul_f32x2(x[i][j], r2), with_offset ? add_f32x2(v[j], o2) : v[j]);
       }
@@ -119,7 +119,7 @@ __device__ __forceinline__ void norm_row(Chunk (&x)[CH], int nch, float inv_n, b
       const int at = threadIdx.x + i * blockDim.x;
       if (FULL || at < nch) {
         Chunk v;
-        unpack_chunk(__ldg(b + at), v);
+        unpack_chunk(fresh(b + at), v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[i][j] = add_f32x2(x[i][j], v[j]);
       }
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(512, CH == 4 ? 2 : 1) norm_kernel(const NormPa
   const bool nvf4 = p.format == QG_NVFP4;
   float g = 1.f;
   if (nvf4) {
-    const float a = __ldg(p.static_amax);
+    const float a = fresh(p.static_amax);
     g = a > 0.f ? __fdiv_rn(a, 2688.f) : 1.f;
     if (m == 0 && threadIdx.x == 0) *p.global_scale = g;
   }

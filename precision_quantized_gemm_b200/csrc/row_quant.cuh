@@ -5,6 +5,7 @@
 // that a mask hides must not reach a sum: 0 * code is 0, 0 * NaN is not).
 #pragma once
 #include "f32x2.cuh"
+#include "loads.cuh"
 #include "ptx.cuh"
 #include "quant_math.cuh"
 

@@ -769,6 +769,43 @@ def test_decoder_step(fmt):
     assert torch.equal(cap[3], o) and torch.equal(cap[5].h, n2.h) and torch.equal(cap[5].operand.q, n2.operand.q)
 
 
+@pytest.mark.parametrize("Hq,n", [(8, 1), (64, 9)])
+def test_rewritten_slots_are_read_afresh(Hq, n):
+    """Writes and reads of the same slots in turn, eager and captured: each call sees what the one before it wrote."""
+    D, Hkv, T, turns = 128, 4, 40, 12
+    g = _gen(8)
+    cache = qg.Cache(qg.QG_FP8_DYNAMIC, 4, 16, Hkv, D)
+    kv = _rand(g, turns, 2, T, Hkv, D)
+    q = _rand(g, n, Hq, D)
+    table = torch.tensor([[2, 0, 3]], dtype=torch.int32, device="cuda")
+    place = torch.arange(T, device="cuda")
+    slots = (table[0, place // 16] * 16 + place % 16).int()
+    offs = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    ws = qg.Workspace("cuda")
+
+    def turn(i, sync):
+        qg.cache_write(cache, kv[i, 0], kv[i, 1], slots)
+        if sync:
+            torch.cuda.synchronize()
+        o = qg.attend(cache, q, offs, lens, table, max_q=n, workspace=ws)
+        if sync:
+            torch.cuda.synchronize()
+        return [o, *qg.cache_read(cache, slots)]
+
+    want = [turn(i, True) for i in range(turns)]
+    got = [turn(i, False) for i in range(turns)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = [turn(i, False) for i in range(turns)]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for w, a, b in zip(want, got, cap):
+            assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(w, a, b))
+
+
 def test_binding_refuses():
     c = qg.Cache(qg.QG_FP8_DYNAMIC, 4, 16, 2, 64)
     k = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
