@@ -69,12 +69,12 @@ __device__ __forceinline__ void rotate(Chunk& x, const uint4& raw, const Turn& r
 // One token per blockIdx.x; its query, key and value rows are dealt to the
 // CTA's groups of L lanes, AHEAD passes of loads at a time: the first are in
 // flight while the turns are formed (8191 tokens of 32 + 2 x 8 heads: 40 us;
-// a pass at a time 43 us, several tokens per CTA 48 to 61 us).
+// a pass at a time 43 us, two 42, six 43; several tokens per CTA 48 to 61 us).
 template <int D, bool INT8>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteParams p) {
   constexpr int L = D / 8;            // lanes per row
   constexpr int ROWS = kThreads / L;  // rows per pass of the CTA
-  constexpr int AHEAD = 3;
+  constexpr int AHEAD = 4;
   __shared__ __align__(16) float turn_c[D / 2], turn_s[D / 2];
   griddep_launch_dependents();
   griddep_wait();
