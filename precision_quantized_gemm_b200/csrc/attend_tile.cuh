@@ -360,6 +360,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
               if (up) m[i] = now;
               l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
             }
+            // what this warp stored before (the tile's earlier weights, and the
+            // accumulator if the reference moved in them) is read back now
+            tmem_st_wait();
             if (!opens) {
 #pragma unroll 1
               for (int d = 0; d < D; d += 16) {
@@ -372,7 +375,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
               }
             }
             if (c > 0) {
-              tmem_st_wait();
 #pragma unroll 1
               for (int d = 0; d < 16 * c; d += 4) {
                 uint32_t w[2];

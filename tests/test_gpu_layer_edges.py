@@ -1,0 +1,38 @@
+"""GPU tests of the layer operators where ordinary inputs do not lead: scores
+that climb, values and queries of extreme scale, weights far below the
+largest, offsets past the end, shared workspaces.  Oracle and tolerances are
+those of the layer parity tests; each test says what it adds to them."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import precision_quantized_gemm_b200 as qg
+from oracle import layer as OL
+from test_gpu_layer import BF16, F16, F32, FMTS, Batch, _cache_values, _close, _cuda, _gen, _np, _rand  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ climbing scores --
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,n,Hq,Hkv", [
+    ([700], 1, 4, 2), ([1500, 333], 3, 8, 2), ([350] * 100, 1, 4, 4),      # few rows; split and whole items
+    ([700], 20, 4, 2), ([1500, 333], 9, 64, 4), ([350] * 100, 9, 16, 4)])  # tiles
+def test_scores_that_climb(fmt, D, lens, n, Hq, Hkv):
+    """Scores that grow by 0 to 20 powers of two with every 32 positions, so that a row's reference moves in
+    neighbouring blocks of one tile: sums, accumulator and earlier weights follow every time."""
+    b = Batch(fmt, lens, [n] * len(lens), Hq, Hkv, D, 16, seed=D + len(lens) + n, tree=False)
+    g = _gen(7 * D + n)
+    total = sum(lens)
+    u = (torch.randint(0, 2, (1, Hkv, D), generator=g, device="cuda") * 2 - 1).float()
+    steps = torch.cat([(20 * torch.rand(-(-a // 32), generator=g, device="cuda")).cumsum(0).repeat_interleave(32)[:a]
+                       for a in lens])
+    steps += 6 * torch.rand(total, generator=g, device="cuda")
+    c = steps / (math.log2(math.e) * math.sqrt(D))
+    qg.cache_write(b.cache, (c[:, None, None] * u).to(torch.bfloat16), _rand(g, total, Hkv, D), b.slots.int())
+    gain = 0.3 + 0.7 * torch.rand(b.T + 3, Hq, 1, generator=g, device="cuda")
+    b.q = (gain * u.repeat_interleave(Hq // Hkv, 1)).to(torch.bfloat16)
+    b.check(*b.run(), rows=2)
