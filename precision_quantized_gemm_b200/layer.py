@@ -245,7 +245,8 @@ def rope_frequencies(dim: int, base: float = 10000.0, scaling: str | None = None
         def index(turns):  # the pair that turns so many times in the original context
             return dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
 
-        first, last = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), dim // 2 - 1)
+        # (the upper end may lie past the last pair, which is then blended, too)
+        first, last = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), dim - 1)
         keep = 1 - ((j - first) / max(last - first, 1e-3)).clamp(0, 1)
         f = f * (keep + (1 - keep) / factor)
         magnitude = 0.1 * math.log(factor) + 1.0
