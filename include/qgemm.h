@@ -511,6 +511,8 @@ qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, 
  * [0, max_pages * page_size], pages to [0, pages); drafted tokens past max_q
  * get no output.  batch <= 1024, max_q <= QGEMM_ATTEND_MAX_Q
  * (QG_ERR_UNSUPPORTED).
+ * A value scale below 2^-80 (values below 4e-22, or a place that was never
+ * written) counts as 2^-80.
  * The queries are exact down to 2^-28 of their row's largest; weights are
  * f16 relative to the largest |weight x value scale|, everything else fp32. */
 typedef struct {

@@ -15,8 +15,9 @@
 // power of two per row brings their largest magnitude to [2^14, 2^15).
 // Sums, maxima and accumulators are fp32.
 //
-// Value scales are held to [2^-110, 2^95] (a smaller row counts as that
-// small: below 4e-31 in magnitude), which keeps 1 / vs and l finite.  A NaN
+// Value scales are held to [2^-80, 2^95] (a smaller row counts as that small:
+// below 4e-22 in magnitude), which keeps l finite: w_j / vs_j is at most 2^88,
+// and 2^31 positions of it stay below fp32's 2^128.  A NaN
 // scale (a row with a NaN or an infinity) makes the rows that see it NaN.
 #pragma once
 #include <cuda_bf16.h>
@@ -31,7 +32,7 @@
 namespace qg {
 
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kVsMin = 7.703719777548943e-34f;  // 2^-110
+constexpr float kVsMin = 8.271806125530277e-25f;  // 2^-80
 constexpr float kVsMax = 3.961408125713217e28f;   // 2^95
 constexpr float kRescaleAt = 8.f;                 // log2: how far a score may pass its row's reference
 

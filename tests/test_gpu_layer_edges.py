@@ -36,3 +36,19 @@ def test_scores_that_climb(fmt, D, lens, n, Hq, Hkv):
     gain = 0.3 + 0.7 * torch.rand(b.T + 3, Hq, 1, generator=g, device="cuda")
     b.q = (gain * u.repeat_interleave(Hq // Hkv, 1)).to(torch.bfloat16)
     b.check(*b.run(), rows=2)
+
+
+# ------------------------------------------------- value scales and weights --
+@pytest.mark.parametrize("Hq", [1, 64])
+@pytest.mark.parametrize("D", [64, 128])
+def test_log_sum_of_zero_scales(Hq, D):
+    """300,000 places that were never written (scales 0): zeros, and the log of their number.  The sum holds the
+    scales' reciprocals: the logarithm's two units in the last place are those of 128 at most, 2^-16."""
+    n, page = 300000, 1024
+    cache = qg.Cache(qg.QG_FP8_DYNAMIC, -(-n // page), page, 1, D)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lse = torch.zeros(1, Hq, device="cuda")
+    table = torch.arange(cache.pages, dtype=torch.int32, device="cuda").view(1, -1)
+    out = qg.attend(cache, _rand(_gen(1), 1, Hq, D), ints(0, 1), ints(n), table, lse=lse)
+    assert not out.any()
+    _close(lse, np.full((1, Hq), math.log(n)), 2.0 ** -15, "lse")
