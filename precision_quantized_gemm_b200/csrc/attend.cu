@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
         }
       if (__any_sync(0xffffffffu, grown)) {
         // a new reference where a row's maximum has passed the old one by more
-        // than 2^8 (weights stay below 256); sums and accumulator follow
+        // than 2^8 (weights stay below 2^15); sums and accumulator follow
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
       uint32_t wb[2][NR][2];  // weights as the second operand of each 16 positions
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        const float ref[2] = {m[i][0] == kNegInf ? 0.f : m[i][0], m[i][1] == kNegInf ? 0.f : m[i][1]};
+        const float ref[2] = {m[i][0] == kNegInf ? 0.f : m[i][0] - kWeightUp, m[i][1] == kNegInf ? 0.f : m[i][1] - kWeightUp};
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
           *reinterpret_cast<uint2*>(p.out + (size_t)(tok0 + tk) * p.ldo + h * D + c0) = *reinterpret_cast<uint2*>(v);
           if (p.lse != nullptr && c0 == 0)
             p.lse[(size_t)(tok0 + tk) * p.q_heads + h] =
-                sum == 0.f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+                sum == 0.f ? kNegInf : (top - kWeightUp + log2f(sum)) * 0.6931471805599453f;
         }
       } else {
         *reinterpret_cast<float4*>(part + row * D + c0) = acc;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(ROWS * WPR * 32) qg_attend_merge_kernel(const 
   if constexpr (CPL == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(v);
   else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(v);
   if (p.lse != nullptr && lane == 0)
-    p.lse[tk * p.q_heads + h] = sum == 0.f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+    p.lse[tk * p.q_heads + h] = sum == 0.f ? kNegInf : (top - kWeightUp + log2f(sum)) * 0.6931471805599453f;
 }
 
 cudaError_t launch_pdl(const void* fn, dim3 grid, int threads, size_t smem, void** args, cudaStream_t st, bool pdl) {

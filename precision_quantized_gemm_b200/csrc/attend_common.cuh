@@ -7,16 +7,19 @@
 // With key codes kc and scale ks, value codes vc and scale vs:
 //   s_j = scale * log2(e) * (q . kc_j) ks_j            (base-2 scores)
 //   t_j = s_j + log2(vs_j),  m: max_j t_j, or less by up to kRescaleAt
-//   w_j = 2^(t_j - m)  in [0, 256],  l = sum_j w_j / vs_j
-//   o   = sum_j w_j vc_j / l,       lse = ln 2 (m + log2 l)
+//   w_j = 2^(t_j - m + 7)  in [0, 2^15],  l = sum_j w_j / vs_j
+//   o   = sum_j w_j vc_j / l,       lse = ln 2 (m - 7 + log2 l)
 // so the value scale rides in the exponent and the weights are f16 (11 bits;
-// bf16 would give them 8): a weight below 2^-24 of the largest adds nothing
-// that bf16 outputs keep.  Codes are exact in f16.  Queries are f16 after a
+// bf16 would give them 8).  l has them in fp32; the products round them to
+// f16, whose step below 2^-14 is 2^-24: each is off by 2^-32 of the largest at
+// most where it is that small (the 7 brings the largest near f16's top), n of
+// them by n 2^-32 of a value, a quarter of bf16's half step for 2^22 positions.
+// Codes are exact in f16.  Queries are f16 after a
 // power of two per row brings their largest magnitude to [2^14, 2^15).
 // Sums, maxima and accumulators are fp32.
 //
 // Value scales are held to [2^-80, 2^95] (a smaller row counts as that small:
-// below 4e-22 in magnitude), which keeps l finite: w_j / vs_j is at most 2^88,
+// below 4e-22 in magnitude), which keeps l finite: w_j / vs_j is at most 2^95,
 // and 2^31 positions of it stay below fp32's 2^128.  A NaN
 // scale (a row with a NaN or an infinity) makes the rows that see it NaN.
 #pragma once
@@ -35,6 +38,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kVsMin = 8.271806125530277e-25f;  // 2^-80
 constexpr float kVsMax = 3.961408125713217e28f;   // 2^95
 constexpr float kRescaleAt = 8.f;                 // log2: how far a score may pass its row's reference
+constexpr float kWeightUp = 7.f;                  // log2 of the weight at the reference
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -36,7 +36,7 @@
 // share: with a walk inlined into each role the warps waited for instructions
 // five times as long as they issued.
 // The accumulator is rescaled only when a row's maximum has grown by more
-// than 2^8 since its reference was taken: weights stay below 256, and sums
+// than 2^8 since its reference was taken: weights stay below 2^15, and sums
 // and accumulator keep the same reference, so the result is unchanged.
 #pragma once
 #include "attend_common.cuh"
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
             }
           }
           // the weights go over the scores, 16 columns for 32: what they cover is read
-          const float ref[2] = {m[0] == kNegInf ? 0.f : -m[0], m[1] == kNegInf ? 0.f : -m[1]};
+          const float ref[2] = {m[0] == kNegInf ? 0.f : kWeightUp - m[0], m[1] == kNegInf ? 0.f : kWeightUp - m[1]};
           uint32_t w[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
                   part[kTileRows * D + row] = m[i];
                   part[kTileRows * D + kTileRows + row] = l[i];
                 } else if (p.lse != nullptr) {
-                  p.lse[tk * p.q_heads + h] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+                  p.lse[tk * p.q_heads + h] = l[i] == 0.f ? kNegInf : (m[i] - kWeightUp + log2f(l[i])) * 0.6931471805599453f;
                 }
               }
               if (whole) {

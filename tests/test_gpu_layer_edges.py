@@ -52,3 +52,38 @@ def test_log_sum_of_zero_scales(Hq, D):
     out = qg.attend(cache, _rand(_gen(1), 1, Hq, D), ints(0, 1), ints(n), table, lse=lse)
     assert not out.any()
     _close(lse, np.full((1, Hq), math.log(n)), 2.0 ** -15, "lse")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 64])
+def test_many_weights_far_below_the_largest(fmt, D, Hq):
+    """One position 25.5 powers of two above 16384 others that it shares a reference with: the others are all that
+    reaches the channels in which its value is 0.  A weight is off by 2^-32 of the largest (f16 near its lowest),
+    the sum of the others by as much for each."""
+    n, page, B, H = 16384, 1024, 300, 2
+    cache = qg.Cache(fmt, n // page, page, H, D)
+    g = _gen(D + Hq)
+    k = torch.zeros(n, H, D, device="cuda", dtype=torch.bfloat16)
+    k[5, :, 0] = 25.5 / math.log2(math.e)
+    v = torch.zeros(n, H, D, device="cuda", dtype=torch.bfloat16)
+    v[:, :, 1] = 1.0
+    v[5, :, 1], v[5, :, 2] = 0.0, 1.0
+    qg.cache_write(cache, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+    # every sequence reads the same pages: enough of them that one CTA has a whole item
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").repeat(B, 1)
+    q = torch.zeros(B, Hq, D, device="cuda", dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    lse = torch.zeros(B, Hq, device="cuda")
+    out = qg.attend(cache, q, torch.arange(B + 1, dtype=torch.int32, device="cuda"),
+                    torch.full((B,), n, dtype=torch.int32, device="cuda"), table, max_q=1, scale=1.0, lse=lse)
+    (kc, ks), (vc, vs) = _cache_values(cache, torch.arange(n, device="cuda"))
+    o, l, mag = OL.attend_one(_np(q[0, 0]), kc[:, 0] * ks[:, :1], vc[:, 0] * vs[:, :1], 1.0, np.ones(n, bool))
+    assert 2.0 ** -12 < o[1] < 2.0 ** -11
+    # exponents of 26 hold 2^-19: the scores' roundings, and the rest as for ordinary inputs
+    rel = F16 + 2.0 ** -17 + n * F32
+    _close(out, np.broadcast_to(o, out.shape), BF16 * np.abs(o) + rel * mag + n * 2.0 ** -32, "out")
+    # the sum is kept in 16 chains or more a row (tiles: 2 groups x 4 lanes x 2 elements), each of at most n / 16
+    # additions that round by half a unit of the sum so far, which is at most the whole: n / 16 F32 of it.  (Beside
+    # the largest, a term of 2^-25.5 of it is under half a unit and lost: 1 / 16 of 16384 x 2^-25.5 is 2.2e-5.)
+    _close(lse, np.full((B, Hq), l), 2.0 ** -17 + n / 16 * F32 + 4 * F32 * abs(l), "lse")
