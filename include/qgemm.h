@@ -512,7 +512,8 @@ qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, 
  * get no output.  batch <= 1024, max_q <= QGEMM_ATTEND_MAX_Q
  * (QG_ERR_UNSUPPORTED).
  * A value scale below 2^-80 (values below 4e-22, or a place that was never
- * written) counts as 2^-80.
+ * written) counts as 2^-80; where those that a token sees lie more than 2^100
+ * apart, the share of the smaller ones may be lost.
  * The queries are exact down to 2^-28 of their row's largest; weights are
  * f16 relative to the largest |weight x value scale|, everything else fp32. */
 typedef struct {

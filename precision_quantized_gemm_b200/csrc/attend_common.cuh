@@ -18,10 +18,13 @@
 // power of two per row brings their largest magnitude to [2^14, 2^15).
 // Sums, maxima and accumulators are fp32.
 //
-// Value scales are held to [2^-80, 2^95] (a smaller row counts as that small:
-// below 4e-22 in magnitude), which keeps l finite: w_j / vs_j is at most 2^95,
-// and 2^31 positions of it stay below fp32's 2^128.  A NaN
+// Value scales are held to [2^-80, 2^125].  A smaller row counts as that small
+// (below 4e-22 in magnitude), which keeps l finite: w_j / vs_j is at most
+// 2^95, and 2^31 positions of it stay below fp32's 2^128.  The upper bound
+// keeps 1 / vs normal; no row of bf16 values reaches it.  A NaN
 // scale (a row with a NaN or an infinity) makes the rows that see it NaN.
+// Where the scales a row sees are more than 2^100 apart, the weight of the
+// smaller ones may underflow, and their share of l with it.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,7 +39,7 @@ namespace qg {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kVsMin = 8.271806125530277e-25f;  // 2^-80
-constexpr float kVsMax = 3.961408125713217e28f;   // 2^95
+constexpr float kVsMax = 4.253529586511731e37f;   // 2^125
 constexpr float kRescaleAt = 8.f;                 // log2: how far a score may pass its row's reference
 constexpr float kWeightUp = 7.f;                  // log2 of the weight at the reference
 

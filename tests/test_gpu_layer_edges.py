@@ -87,3 +87,17 @@ def test_many_weights_far_below_the_largest(fmt, D, Hq):
     # additions that round by half a unit of the sum so far, which is at most the whole: n / 16 F32 of it.  (Beside
     # the largest, a term of 2^-25.5 of it is under half a unit and lost: 1 / 16 of 16384 x 2^-25.5 is 2.2e-5.)
     _close(lse, np.full((B, Hq), l), 2.0 ** -17 + n / 16 * F32 + 4 * F32 * abs(l), "lse")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("Hq,n", [(4, 1), (64, 3)])
+def test_values_near_the_top_of_bf16(fmt, Hq, n):
+    """Values up to 2^127, whose scales pass 2^95."""
+    b = Batch(fmt, [300, 77], [n, 1], Hq, 2, 64, 16, seed=3)
+    g = _gen(9)
+    total = sum(b.lens)
+    v = 2.0 * torch.rand(total, 2, 64, generator=g, device="cuda") - 1.0
+    v *= 2.0 ** (102 + 25 * torch.rand(total, 1, 1, generator=g, device="cuda"))
+    qg.cache_write(b.cache, _rand(g, total, 2, 64), v.to(torch.bfloat16), b.slots.int())
+    assert b.cache.v_scale.view(-1)[b.cache.v_scale.view(-1).isfinite()].max() > 2.0 ** 110
+    b.check(*b.run())
