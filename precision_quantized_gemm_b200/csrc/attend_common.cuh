@@ -262,11 +262,12 @@ __device__ __forceinline__ void value_scale(float vs, float& log2_vs, float& inv
   log2_vs = vs - vs == 0.f ? lg : __uint_as_float(0x7fc00000u);
 }
 
-// Power of two that brings a row's largest magnitude to [2^14, 2^15), and its
-// inverse; 1 for a zero row or one with an infinity.
+// Power of two that brings a row's largest magnitude to [2^14, 2^15) (below
+// 2^-112: as near as 2^126 brings it), and its inverse; 1 for a zero row or
+// one with an infinity.  Both are normal.
 __device__ __forceinline__ void row_power(float amax, float& up, float& down) {
   const int e = (int)(__float_as_uint(amax) >> 23) & 0xff;
-  const int shift = amax > 0.f && e < 255 ? min(max(14 + 127 - e, -100), 100) : 0;
+  const int shift = amax > 0.f && e < 255 ? min(14 + 127 - e, 126) : 0;
   up = __uint_as_float((uint32_t)(127 + shift) << 23);
   down = __uint_as_float((uint32_t)(127 - shift) << 23);
 }

@@ -101,3 +101,14 @@ def test_values_near_the_top_of_bf16(fmt, Hq, n):
     qg.cache_write(b.cache, _rand(g, total, 2, 64), v.to(torch.bfloat16), b.slots.int())
     assert b.cache.v_scale.view(-1)[b.cache.v_scale.view(-1).isfinite()].max() > 2.0 ** 110
     b.check(*b.run())
+
+
+@pytest.mark.parametrize("power", [122, -124])
+@pytest.mark.parametrize("Hq,n", [(4, 1), (64, 3)])
+def test_queries_at_the_ends_of_bf16(Hq, n, power):
+    """Queries of 2^122 and of 2^-124 times ordinary ones, with a softmax scale that brings them back."""
+    b = Batch(qg.QG_W8A8_INT8, [300, 77], [n, 1], Hq, 2, 64, 16, seed=3)
+    b.q = (b.q.double() * 2.0 ** power).to(torch.bfloat16)
+    assert b.q.isfinite().all() and b.q.abs().max() > 2.0 ** (power + 1)
+    scale = 0.125 * 2.0 ** -power
+    b.check(*b.run(scale=scale), scale=scale)
