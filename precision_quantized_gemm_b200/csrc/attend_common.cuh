@@ -6,14 +6,15 @@
 // query heads that share a key head are stacked (row = token * group + head).
 // With key codes kc and scale ks, value codes vc and scale vs:
 //   s_j = scale * log2(e) * (q . kc_j) ks_j            (base-2 scores)
-//   t_j = s_j + log2(vs_j),  m: max_j t_j, or less by up to kRescaleAt
+//   t_j = s_j + log2(vs_j),  m: max_j t_j, or less by up to kRescaleAt (tiles:
+//                            also more, by up to 1)
 //   w_j = 2^(t_j - m + 7)  in [0, 2^15],  l = sum_j w_j / vs_j
 //   o   = sum_j w_j vc_j / l,       lse = ln 2 (m - 7 + log2 l)
 // so the value scale rides in the exponent and the weights are f16 (11 bits;
 // bf16 would give them 8).  l has them in fp32; the products round them to
-// f16, whose step below 2^-14 is 2^-24: each is off by 2^-32 of the largest at
+// f16, whose step below 2^-14 is 2^-24: each is off by 2^-31 of the largest at
 // most where it is that small (the 7 brings the largest near f16's top), n of
-// them by n 2^-32 of a value, a quarter of bf16's half step for 2^22 positions.
+// them by n 2^-31 of a value, half of bf16's half step for 2^22 positions.
 // Codes are exact in f16.  Queries are f16 after a
 // power of two per row brings their largest magnitude to [2^14, 2^15).
 // Sums, maxima and accumulators are fp32.

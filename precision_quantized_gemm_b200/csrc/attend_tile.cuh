@@ -38,6 +38,9 @@
 // The accumulator is rescaled only when a row's maximum has grown by more
 // than 2^8 since its reference was taken: weights stay below 2^15, and sums
 // and accumulator keep the same reference, so the result is unchanged.
+// References are whole numbers: the factors are powers of two, and the f16
+// weights that a tile already has take them without a second rounding (but
+// for those that leave f16's normal range: 2^-32 of the largest, as above).
 #pragma once
 #include "attend_common.cuh"
 #include "f32x2.cuh"
@@ -356,6 +359,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
               now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 1));
               now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 2));
               const bool up = now > m[i] + kRescaleAt;
+              now = ceilf(now);  // references are whole, factors powers of two
               f[i] = up ? ex2(m[i] - now) : 1.f;  // m = -inf: 0
               if (up) m[i] = now;
               l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));

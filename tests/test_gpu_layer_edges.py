@@ -112,3 +112,41 @@ def test_queries_at_the_ends_of_bf16(Hq, n, power):
     assert b.q.isfinite().all() and b.q.abs().max() > 2.0 ** (power + 1)
     scale = 0.125 * 2.0 ** -power
     b.check(*b.run(scale=scale), scale=scale)
+
+
+def test_weights_are_rounded_once():
+    """A tile whose third 16 positions raise the reference by some ten powers of two: the f16 weights that it has by
+    then follow without a second rounding.  Two positions of nearly the same weight and opposite values leave the
+    roundings' difference; what raises the references has values of 0."""
+    B, H, G, D, page = 128, 4, 40, 64, 16
+    r = np.random.default_rng(0)
+    cache = qg.Cache(qg.QG_FP8_DYNAMIC, 4 * B, page, H, D)
+    score = np.full((B, H, 64), -200.0)          # base 2
+    score[:, :, 3] = 0.0                         # the first reference
+    a, b, c = r.uniform(-2.99, -2.9, (B, H)), 9, 40
+    score[:, :, 5] = a
+    score[:, :, b] = a + r.uniform(-0.002, 0.002, (B, H))
+    score[:, :, c] = r.uniform(9.0, 10.0, (B, H)) - 0.02
+    # keys: code +-1 in channel 0, the scale says how much
+    k_scale = torch.from_numpy(np.abs(score) / math.log2(math.e)).float().cuda().view(B, H, 4, page).transpose(1, 2)
+    cache.k_scale.copy_(k_scale.reshape(4 * B, H, page))
+    sign = torch.from_numpy(np.where(score < 0, 0xb8, 0x38).astype(np.uint8)).cuda().view(B, H, 4, page).transpose(1, 2)
+    cache.k[..., 0] = sign.reshape(4 * B, H, page)
+    cache.v_scale.fill_(1.0)
+    v = torch.zeros(B, H, 64, dtype=torch.uint8, device="cuda")
+    v[:, :, 5], v[:, :, b] = 0x38, 0xb8
+    cache.v.copy_(v.view(B, H, 4, page).transpose(1, 2).reshape(4 * B, H, page)[..., None].expand(-1, -1, -1, D))
+    q = torch.zeros(B, H * G, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    ints = lambda x: x.to(dtype=torch.int32, device="cuda")  # noqa: E731
+    out = qg.attend(cache, q, ints(torch.arange(B + 1)), ints(torch.full((B,), 64)),
+                    ints(torch.arange(4 * B)).view(B, 4), max_q=1, scale=1.0)
+    # the scores as the scales hold them
+    z = np.sign(score) * _np(cache.k_scale.view(B, 4, H, page).transpose(1, 2).reshape(B, H, 64))
+    p = np.exp(z - z.max(axis=2, keepdims=True))
+    p /= p.sum(axis=2, keepdims=True)
+    want, mag = p[:, :, 5] - p[:, :, b], p[:, :, 5] + p[:, :, b]
+    # one rounding to f16 a weight; scores of 10 in fp32, a few roundings and the exponential: 2^-18
+    tol = BF16 * np.abs(want) + (F16 + 2.0 ** -18) * mag
+    wide = lambda x: np.broadcast_to(x[:, :, None, None], (B, H, G, D))  # noqa: E731
+    _close(out.view(B, H, G, D), wide(want), wide(tol), "out")
