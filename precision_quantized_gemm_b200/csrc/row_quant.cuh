@@ -49,13 +49,14 @@ __device__ __forceinline__ float absmax_chunk(const Chunk& x) {
   return absmax_nan(absmax_nan(m[0], m[1]), absmax_nan(m[2], m[3]));
 }
 
-// Scale of a row, and its reciprocal: correctly rounded, or 0 where it would
-// overflow (a scale below the normal range).  An operand's scale is the
+// Scale of a row, and its reciprocal: correctly rounded, or 0 for a scale below
+// kSmallScale, whose codes are divided.  An operand's scale is the
 // quantisers' divided one.  A cached row's (CACHED) is the product with the
 // rounded 1 / 448 or 1 / 127, which is how a division by a constant is
 // computed for tensors: the two differ by a unit in the last place at most,
 // but bf16 values lie on the ties of the codes often (1 in 16 where amax is
 // 1.75 times a power of two), and a tie goes the way its scale leans.
+constexpr float kSmallScale = 8.077935669463161e-28f;  // 2^-90
 template <bool INT8, bool CACHED>
 __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
   amax = fabsf(amax);
@@ -65,18 +66,21 @@ __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
   } else {
     if constexpr (CACHED) s = amax > 0.f ? __fmul_rn(amax, 1.f / (INT8 ? 127.f : 448.f)) : 1.f;
     else s = scale_of_amax<INT8>(amax);
-    inv = s >= 1.17549435e-38f ? __fdiv_rn(1.f, s) : 0.f;
+    inv = s >= kSmallScale ? __fdiv_rn(1.f, s) : 0.f;
   }
 }
 
 // Codes of 8 values, low byte first: round(x / s), as quant8 gives them; all
 // zero for a row whose scale is NaN.
-// The quotient is q = x inv, improved by its own remainder: with inv the
-// correctly rounded 1 / s and r = x - q s exact (fma), q + r inv is x / s to
-// 2^-46 before its one rounding, so the code is that of the divided quotient
-// (the plain product is not: it leaves the tie on one side or the other, and
-// bf16 values over amax / 127 are ties often).  Three two-wide instructions
-// for two values, where the division takes some twenty.
+// The quotient is q = x inv, improved by its own remainder (P. Markstein's
+// division, IBM J. Res. Dev. 34, 1990): with inv the correctly rounded 1 / s,
+// q within a unit of x / s and r = x - q s exact (fma), q + r inv rounds as
+// the division does.  (The plain product does not: it leaves the tie on one
+// side or the other, and bf16 values over amax / 127 are ties often.)  Three
+// two-wide instructions for two values.
+// r is exact while its last bit, 2^-46 of q s, is one that fp32 has: the
+// smallest quotient that is not far below every tie is 2^-10 (e4m3), so
+// s >= 2^-149 + 46 + 10 = 2^-93 is enough.  Rows below 2^-90 are divided.
 template <bool INT8>
 __device__ __forceinline__ uint2 chunk_codes(const Chunk& x, float s, float inv) {
   if (s != s) return make_uint2(0u, 0u);

@@ -150,3 +150,36 @@ def test_weights_are_rounded_once():
     tol = BF16 * np.abs(want) + (F16 + 2.0 ** -18) * mag
     wide = lambda x: np.broadcast_to(x[:, :, None, None], (B, H, G, D))  # noqa: E731
     _close(out.view(B, H, G, D), wide(want), wide(tol), "out")
+
+
+# -------------------------------------------------------- codes of tiny rows --
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("power", [-126, -120, -114, -100, -94, -88, -60])
+def test_codes_of_tiny_rows_are_the_quotients(fmt, power):
+    """fp32 rows (bf16 times a magnitude, unrotated at position 0) next to the ties of their codes, with scales
+    from 2^-126 up: the codes are those of the correctly rounded quotient, also where the remainder that corrects
+    it would underflow."""
+    g = _gen(power + 200)
+    T, D, top = 256, 64, 127.0 if fmt == qg.QG_W8A8_INT8 else 448.0
+    if fmt == qg.QG_W8A8_INT8:
+        x = (2 * torch.randint(0, 127, (T, 1, D), generator=g, device="cuda") + 1) / 2
+    else:
+        x = (1 + (2 * torch.randint(0, 8, (T, 1, D), generator=g, device="cuda") + 1) / 16) * 2.0 ** torch.randint(
+            -6, 8, (T, 1, D), generator=g, device="cuda")
+    x[:, :, 0] = top
+    k = (x.double() * 2.0 ** power).to(torch.bfloat16)
+    zeros = torch.zeros(T, dtype=torch.int32, device="cuda")
+    freq = qg.rope_frequencies(D)[0]
+    cache = qg.Cache(fmt, T // 16, 16, 1, D)
+    one = torch.ones((), device="cuda")
+    for i in range(8):
+        magnitude = (1 + torch.rand(1, generator=g, device="cuda")).item()
+        qg.cache_write(cache, k, k, torch.arange(T, dtype=torch.int32, device="cuda"), positions=zeros,
+                       rope=qg.Rope(freq, magnitude=magnitude))
+        y = (k.double() * torch.tensor(magnitude).float().double().item()).float().view(T, D)
+        scale = y.abs().amax(-1) * (one / top)
+        assert torch.equal(cache.k_scale.view(-1), scale)
+        quotient = (y.double() / scale.double()[:, None]).float()
+        want = quotient.round().to(torch.int8) if fmt == qg.QG_W8A8_INT8 else quotient.to(torch.float8_e4m3fn)
+        same = cache.k.view(-1, D) == want.view(torch.uint8)
+        assert same.all(), (i, int((~same).sum()))
