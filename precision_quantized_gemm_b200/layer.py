@@ -7,7 +7,7 @@ in the package's own module; the formulas stand in include/qgemm.h.
     qkv = run(QG_FP8_DYNAMIC, r.operand, Wqkv).view(T, Hq + 2 * Hkv, D)
     q, k, v = qkv.split([Hq, Hkv, Hkv], 1)
     q = cache_write(cache, k, v, slots, q=q, rope=rope, positions=positions)
-    o = attend(cache, q, q_offsets, kv_len, page_table, tree_mask=mask)
+    o = attend(cache, q, q_offsets, kv_len, page_table, tree_mask=mask, max_q=most)
 
 Shapes, types and strides are checked here (ValueError); sizes, alignment and
 options by the library (QGemmError).  ``stream``: the torch stream to launch
@@ -360,7 +360,8 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
     positions, those tokens' own (already written) included; page_table int32
     [B, max_pages].  tree_mask int64 [T, words]: bit j of a token's words says
     whether it sees its sequence's drafted token j (None: causal).  max_q: the
-    most tokens of one sequence (default: the most that T allows).  scale:
+    most tokens of one sequence, at most 256; a sequence's tokens past it get
+    no output (default: T, refused above 256).  scale:
     default head_dim ** -0.5.  lse: fp32 [T, q_heads] buffer for the log sums.
     Returns out (bf16
     [T, q_heads, head_dim]); rows that belong to no sequence are not written."""
@@ -369,6 +370,11 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
     T, Hq, D = q.shape
     B, pages = page_table.shape
     dev = cache.device
+    if max_q is None:
+        # the lengths are on the device: one sequence may have all tokens
+        if T > QGEMM_ATTEND_MAX_Q:
+            raise ValueError(f"more than {QGEMM_ATTEND_MAX_Q} tokens: max_q, the most of one sequence, wanted")
+        max_q = T
     if not _ready(dev, stream):
         with _there(dev, stream):
             return attend(cache, q, q_offsets, kv_len, page_table, tree_mask=tree_mask, scale=scale, max_q=max_q,
@@ -378,7 +384,7 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
                   q=q.data_ptr(), out=out.data_ptr(), q_offsets=_ints("q_offsets", q_offsets, (B + 1,), dev),
                   kv_len=_ints("kv_len", kv_len, (B,), dev), page_table=_ints("page_table", page_table, (B, pages), dev),
                   q_heads=Hq, batch=B, tokens=T, max_pages=pages,
-                  max_q=min(T, QGEMM_ATTEND_MAX_Q) if max_q is None else max_q,
+                  max_q=max_q,
                   scale=D ** -0.5 if scale is None else scale)
     if lse is not None:
         a.lse = _ints("lse", lse, (T, Hq), dev, torch.float32)

@@ -183,3 +183,14 @@ def test_codes_of_tiny_rows_are_the_quotients(fmt, power):
         want = quotient.round().to(torch.int8) if fmt == qg.QG_W8A8_INT8 else quotient.to(torch.float8_e4m3fn)
         same = cache.k.view(-1, D) == want.view(torch.uint8)
         assert same.all(), (i, int((~same).sum()))
+
+
+# ------------------------------------------------------------ number of tokens --
+def test_max_q_left_out():
+    """Every token of every sequence up to 256 in all; 257 of one sequence are refused, not cut."""
+    for lens, ns in (([300], [253]), ([40, 300, 20], [9, 200, 1])):
+        b = Batch(qg.QG_FP8_DYNAMIC, lens, ns, 2, 2, 64, 16, seed=1, tree=False)
+        b.check(*b.run(max_q=None), rows=8)
+    b = Batch(qg.QG_FP8_DYNAMIC, [300], [254], 2, 2, 64, 16, seed=1, tree=False)
+    with pytest.raises(ValueError, match="max_q"):
+        b.run(max_q=None)

@@ -1,0 +1,22 @@
+"""What the binding of the layer operators refuses, and what it hands the library, without a GPU."""
+import pytest
+import torch
+
+import precision_quantized_gemm_b200 as qg
+
+
+def _call(T=3, B=1, Hq=2, **kw):
+    """attend on CPU tensors: refused for the device unless something else is refused before."""
+    cache = qg.Cache(qg.QG_FP8_DYNAMIC, 2, 16, 1, 64, device="cpu")
+    ints = lambda *shape: torch.zeros(*shape, dtype=torch.int32)  # noqa: E731
+    return qg.attend(cache, torch.zeros(T, Hq, 64, dtype=torch.bfloat16), ints(B + 1), ints(B), ints(B, 2), **kw)
+
+
+def test_tokens_past_the_default_max_q():
+    """Without max_q any sequence may have every token: more than the library takes are not cut silently."""
+    with pytest.raises(ValueError, match="max_q"):
+        _call(T=qg.QGEMM_ATTEND_MAX_Q + 1)
+    with pytest.raises(ValueError, match="CUDA"):
+        _call(T=qg.QGEMM_ATTEND_MAX_Q)
+    with pytest.raises(ValueError, match="CUDA"):
+        _call(T=qg.QGEMM_ATTEND_MAX_Q + 1, max_q=1)
