@@ -656,22 +656,22 @@ cudaError_t launch_merge(const AttendParams& p, int tile_rows, int ctas, cudaStr
 // kernel's is that of 128 for any number.  16 sequences of up to 8000
 // positions, 8 key heads of 128: 24 rows 72 us against 88, 32 rows 95 (two
 // items of 16, or one that spills) against 90.
-int tile_rows_of(int rows_max, int head_dim) {
-  const int rows = rows_max <= 8 ? 8 : (rows_max + 7) / 8 * 8;
+int tile_rows_of(int wanted, int head_dim) {
+  const int rows = wanted <= 8 ? 8 : (wanted + 7) / 8 * 8;
   return rows <= (head_dim == 64 ? 32 : 24) ? rows : kTileRows;
 }
 
 }  // namespace
 
-bool attend_tiles(int rows_max, int head_dim) { return tile_rows_of(rows_max, head_dim) == kTileRows; }
+bool attend_tiles(int rows, int head_dim) { return tile_rows_of(rows, head_dim) == kTileRows; }
 
 size_t attend_workspace(int head_dim, int rows_max, int sms) {
   return sizeof(MergeRecord) * sms + (size_t)2 * sms * tile_rows_of(rows_max, head_dim) * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
-                          const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl) {
-  const int rows = tile_rows_of(p.max_q * p.group, head_dim);
+                          const CUtensorMap* tv, int rows, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl) {
+  rows = tile_rows_of(rows, head_dim);
   p.records = static_cast<MergeRecord*>(workspace);
   p.partial = reinterpret_cast<float*>(p.records + sms);
   cudaError_t e;

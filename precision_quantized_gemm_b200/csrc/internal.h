@@ -114,9 +114,9 @@ struct AttendParams {
 };
 constexpr int kAttendMaxBatch = 1024;
 size_t attend_workspace(int head_dim, int rows_max, int sms);
-bool attend_tiles(int rows_max, int head_dim);  // whether the tile kernel takes so many rows per key head
+bool attend_tiles(int rows, int head_dim);  // whether the tile kernel takes so many rows per key head
 cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
-                          const CUtensorMap* tv, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl);
+                          const CUtensorMap* tv, int rows, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl);
 
 // GEMM launchers, one per format (each in its own translation unit).
 // Returns cudaErrorInvalidValue for a (swap, tile_n) pair not instantiated.

@@ -194,3 +194,16 @@ def test_max_q_left_out():
     b = Batch(qg.QG_FP8_DYNAMIC, [300], [254], 2, 2, 64, 16, seed=1, tree=False)
     with pytest.raises(ValueError, match="max_q"):
         b.run(max_q=None)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("ns,Hq,Hkv,D", [([40] + [1] * 30, 16, 2, 128), ([1] * 20 + [0, 33, 0] + [2] * 20, 8, 1, 64),
+                                         ([100, 90, 1, 1], 4, 4, 64), ([130] + [1] * 9, 8, 8, 128)])
+def test_long_and_short_together(fmt, tree, ns, Hq, Hkv, D):
+    """Single tokens next to sequences of many: the mean says which kernel, either takes them all.  max_q as it is,
+    and left out."""
+    lens = [n + 17 * i % 300 for i, n in enumerate(ns)]
+    b = Batch(fmt, lens, ns, Hq, Hkv, D, 16, seed=sum(ns) + D, tree=tree)
+    b.check(*b.run(), rows=3)
+    b.check(*b.run(max_q=None), rows=3)
