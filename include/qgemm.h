@@ -533,7 +533,9 @@ typedef struct {
 } qg_attend;
 
 /* Scratch bytes of qgemm_attend (needs no clearing; calls that may overlap on
- * the GPU each need their own). */
+ * the GPU each need their own).  It is left with any bytes: before a
+ * reduce_mode-2 qgemm_run uses the same memory, clear it
+ * (qgemm_workspace_clear). */
 size_t qgemm_attend_workspace_size(const qg_cache* c, const qg_attend* a);
 qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, size_t ws_bytes, void* stream);
 

@@ -514,18 +514,29 @@ def quantize_weight(fmt: int, W, stream=None) -> Operand:
 
 
 class Workspace:
-    """A zeroed run workspace that grows on demand."""
+    """A run workspace that grows on demand: zeroed for the products, whose
+    counters start at zero, and apart from it a scratch buffer for attend,
+    which leaves any bytes behind.  ``buf``: the buffer handed out last."""
 
     def __init__(self, device="cuda"):
         self.device = device
-        self.buf = None
+        self.buf = self._zeroed = self._scratch = None
 
     def get(self, nbytes: int):
         torch = _torch()
         if nbytes == 0:
             return None, 0
-        if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        if self._zeroed is None or self._zeroed.numel() < nbytes:
+            self._zeroed = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.buf = self._zeroed
+        return self.buf.data_ptr(), self.buf.numel()
+
+    def scratch(self, nbytes: int):
+        """Uninitialised bytes."""
+        torch = _torch()
+        if self._scratch is None or self._scratch.numel() < nbytes:
+            self._scratch = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
+        self.buf = self._scratch
         return self.buf.data_ptr(), self.buf.numel()
 
 

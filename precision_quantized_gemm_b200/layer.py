@@ -395,6 +395,6 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
         a.tree_mask = _ints("tree_mask", tree_mask, (T, a.mask_words), dev, torch.int64)
     L = lib()
     workspace = workspace or Workspace(dev)
-    wsp, wsb = workspace.get(L.qgemm_attend_workspace_size(cache.c, a))
+    wsp, wsb = workspace.scratch(L.qgemm_attend_workspace_size(cache.c, a))
     check(L.qgemm_attend(cache.c, a, wsp, wsb, _here(dev)), "qgemm_attend")
     return out

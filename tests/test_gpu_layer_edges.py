@@ -207,3 +207,21 @@ def test_long_and_short_together(fmt, tree, ns, Hq, Hkv, D):
     b = Batch(fmt, lens, ns, Hq, Hkv, D, 16, seed=sum(ns) + D, tree=tree)
     b.check(*b.run(), rows=3)
     b.check(*b.run(max_q=None), rows=3)
+
+
+# -------------------------------------------------------------------- workspaces --
+@pytest.mark.parametrize("Hq,n", [(8, 1), (64, 9)])
+def test_one_workspace_for_attention_and_products(Hq, n):
+    """A split-K product whose counters have to start at zero, on the workspace that an attention has used."""
+    b = Batch(qg.QG_FP8_DYNAMIC, [900, 1200], [n, n], Hq, 4, 128, 16, seed=2)
+    g = _gen(3)
+    A = qg.quantize_act(qg.QG_FP8_DYNAMIC, _rand(g, 16, 4096))
+    W = qg.quantize_weight(qg.QG_FP8_DYNAMIC, _rand(g, 512, 4096))
+    cfg = qg.make_config(split_k=4, swap_ab=1, tile_n=16, stages=4, reduce_mode=2)
+    want, want_y = b.run(), qg.run(qg.QG_FP8_DYNAMIC, A, W, cfg)
+    ws = qg.Workspace("cuda")
+    for _ in range(3):
+        got = b.run(workspace=ws)
+        y = torch.full_like(want_y, float("nan"))
+        qg.run(qg.QG_FP8_DYNAMIC, A, W, cfg, out=y, workspace=ws)
+        assert torch.equal(y, want_y) and all(torch.equal(u, w) for u, w in zip(got, want))

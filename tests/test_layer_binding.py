@@ -20,3 +20,15 @@ def test_tokens_past_the_default_max_q():
         _call(T=qg.QGEMM_ATTEND_MAX_Q)
     with pytest.raises(ValueError, match="CUDA"):
         _call(T=qg.QGEMM_ATTEND_MAX_Q + 1, max_q=1)
+
+
+def test_scratch_is_apart_from_the_zeroed_workspace():
+    """What attend leaves in its scratch buffer never reaches a product's counters, in either order and growing."""
+    ws = qg.Workspace("cpu")
+    for nbytes in (64, 256, 128, 1024):
+        p, n = ws.scratch(nbytes)
+        assert n >= nbytes and ws.buf.data_ptr() == p
+        ws.buf.fill_(0xff)
+        z, m = ws.get(nbytes)
+        assert m >= nbytes and z != p and ws.buf.data_ptr() == z and not ws.buf.any()
+    assert ws.get(0) == (None, 0)
