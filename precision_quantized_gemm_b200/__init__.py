@@ -521,6 +521,7 @@ class Workspace:
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = self._zeroed = self._scratch = None
+        self._outgrown = []
 
     def get(self, nbytes: int):
         torch = _torch()
@@ -532,9 +533,11 @@ class Workspace:
         return self.buf.data_ptr(), self.buf.numel()
 
     def scratch(self, nbytes: int):
-        """Uninitialised bytes."""
+        """Uninitialised bytes.  A buffer that a larger one replaces is kept: a captured graph may use it (20 MB at most)."""
         torch = _torch()
         if self._scratch is None or self._scratch.numel() < nbytes:
+            if self._scratch is not None:
+                self._outgrown.append(self._scratch)
             self._scratch = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
         self.buf = self._scratch
         return self.buf.data_ptr(), self.buf.numel()

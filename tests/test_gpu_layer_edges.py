@@ -225,3 +225,23 @@ def test_one_workspace_for_attention_and_products(Hq, n):
         y = torch.full_like(want_y, float("nan"))
         qg.run(qg.QG_FP8_DYNAMIC, A, W, cfg, out=y, workspace=ws)
         assert torch.equal(y, want_y) and all(torch.equal(u, w) for u, w in zip(got, want))
+
+
+def test_a_graph_keeps_its_workspace():
+    """A captured call replayed after a larger one has made the shared workspace grow."""
+    b = Batch(qg.QG_W8A8_INT8, [3000], [1], 8, 2, 64, 64, seed=3, tree=False)
+    c = Batch(qg.QG_FP8_DYNAMIC, [900, 1200], [9, 9], 64, 4, 128, 16, seed=2)
+    ws = qg.Workspace("cuda")
+    want = b.run(workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = b.run(workspace=ws)
+    small = ws.buf.numel()
+    c.run(workspace=ws)
+    assert ws.buf.numel() > small
+    other = [torch.zeros(small, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for t in got:
+        t.fill_(3)
+    graph.replay()
+    assert all(torch.equal(u, w) for u, w in zip(got, want)) and not any(t.any() for t in other)

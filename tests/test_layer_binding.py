@@ -32,3 +32,14 @@ def test_scratch_is_apart_from_the_zeroed_workspace():
         z, m = ws.get(nbytes)
         assert m >= nbytes and z != p and ws.buf.data_ptr() == z and not ws.buf.any()
     assert ws.get(0) == (None, 0)
+
+
+def test_an_outgrown_scratch_buffer_stays():
+    """A captured graph holds its address."""
+    ws = qg.Workspace("cpu")
+    ws.scratch(64)
+    first = ws.buf
+    ws.scratch(128)
+    assert ws.buf is not first and any(t is first for t in ws._outgrown)
+    ws.scratch(64)
+    assert len(ws._outgrown) == 1
