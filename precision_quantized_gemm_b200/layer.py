@@ -367,6 +367,8 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
     [T, q_heads, head_dim]); rows that belong to no sequence are not written."""
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("q: bf16 [tokens, q_heads, head_dim], page_table: int32 [batch, max_pages] wanted")
+    if tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[1] == 0):
+        raise ValueError("tree_mask: int64 [tokens, words], at least one word, wanted")
     T, Hq, D = q.shape
     B, pages = page_table.shape
     dev = cache.device
@@ -389,8 +391,6 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
     if lse is not None:
         a.lse = _ints("lse", lse, (T, Hq), dev, torch.float32)
     if tree_mask is not None:
-        if tree_mask.dim() != 2:
-            raise ValueError("tree_mask: int64 [tokens, words] wanted")
         a.mask_words = tree_mask.shape[1]
         a.tree_mask = _ints("tree_mask", tree_mask, (T, a.mask_words), dev, torch.int64)
     L = lib()

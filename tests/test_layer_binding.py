@@ -43,3 +43,13 @@ def test_an_outgrown_scratch_buffer_stays():
     assert ws.buf is not first and any(t is first for t in ws._outgrown)
     ws.scratch(64)
     assert len(ws._outgrown) == 1
+
+
+def test_a_mask_without_words_is_refused():
+    """Its address is null, which the library reads as no mask: causal, where the caller means nothing drafted."""
+    with pytest.raises(ValueError, match="tree_mask"):
+        _call(tree_mask=torch.zeros(3, 0, dtype=torch.int64))
+    with pytest.raises(ValueError, match="tree_mask"):
+        _call(tree_mask=torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="CUDA"):
+        _call(tree_mask=torch.zeros(3, 1, dtype=torch.int64))
