@@ -163,6 +163,8 @@ def norm(residual, weight, x=None, *, bias=None, kind="rms", post_weight=None, p
         y = first.new_empty((M, N))
     if fmt is not None and out is None:
         out = _operand(fmt, M, N, dev)
+    elif out is not None and out.q.device != dev:
+        raise ValueError(f"out: an operand on {dev} wanted")
     a = qg_norm(residual_scale=residual_scale, block_scale=block_scale, eps=eps, weight_offset=weight_offset)
     if residual is not None:
         a.ldr, a.residual = _rows("residual", residual, M, N, dev), residual.data_ptr()
@@ -396,5 +398,7 @@ def attend(cache: Cache, q, q_offsets, kv_len, page_table, *, tree_mask=None, sc
     L = lib()
     workspace = workspace or Workspace(dev)
     wsp, wsb = workspace.scratch(L.qgemm_attend_workspace_size(cache.c, a))
+    if workspace.buf.device != dev:
+        raise ValueError(f"workspace: one on {dev} wanted")
     check(L.qgemm_attend(cache.c, a, wsp, wsb, _here(dev)), "qgemm_attend")
     return out

@@ -245,3 +245,13 @@ def test_a_graph_keeps_its_workspace():
         t.fill_(3)
     graph.replay()
     assert all(torch.equal(u, w) for u, w in zip(got, want)) and not any(t.any() for t in other)
+
+
+def test_buffers_of_another_device_are_refused():
+    """An operand or a workspace in host memory never reaches a kernel."""
+    x, w = _rand(_gen(0), 3, 128), _rand(_gen(1), 128)
+    with pytest.raises(ValueError, match="operand"):
+        qg.norm(x, w, out=qg.Operand(qg.QG_FP8_DYNAMIC, False, 3, 128, "cpu"))
+    b = Batch(qg.QG_FP8_DYNAMIC, [20], [1], 2, 2, 64, 16, seed=1, tree=False)
+    with pytest.raises(ValueError, match="workspace"):
+        b.run(workspace=qg.Workspace("cpu"))
