@@ -89,13 +89,20 @@ def _here(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _stride(name, stride):
+    # the structures' strides are 32-bit, and ctypes would cut a larger one
+    if stride > 0x7fffffff:
+        raise ValueError(f"{name}: a row stride below 2^31 elements wanted")
+    return stride
+
+
 def _rows(name, t, rows, width, device):
     """A bf16 matrix [rows, width] with contiguous rows; its row stride."""
     if t.dtype != torch.bfloat16 or t.shape != (rows, width) or t.device != device:
         raise ValueError(f"{name}: bf16 [{rows}, {width}] on {device} wanted")
     if width > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return t.stride(0) if rows > 1 else width
+    return _stride(name, t.stride(0)) if rows > 1 else width
 
 
 def _heads(name, t, tokens, heads, dim, device):
@@ -105,7 +112,7 @@ def _heads(name, t, tokens, heads, dim, device):
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: a token's heads must lie side by side")
-    return st[0] if tokens > 1 else heads * dim
+    return _stride(name, st[0]) if tokens > 1 else heads * dim
 
 
 def _ints(name, t, shape, device, dtype=None):

@@ -53,3 +53,18 @@ def test_a_mask_without_words_is_refused():
         _call(tree_mask=torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ValueError, match="CUDA"):
         _call(tree_mask=torch.zeros(3, 1, dtype=torch.int64))
+
+
+def test_strides_past_32_bits_are_refused():
+    """A row stride of 2^32 + 256 elements is not one of 256."""
+    from precision_quantized_gemm_b200 import layer
+    with pytest.raises(ValueError, match="CUDA"):
+        _call()  # (the module's torch is there from the first call on)
+    far = torch.empty(1, dtype=torch.bfloat16, device="meta").as_strided((2, 256), ((1 << 32) + 256, 1))
+    with pytest.raises(ValueError, match="stride"):
+        layer._rows("x", far, 2, 256, far.device)
+    with pytest.raises(ValueError, match="stride"):
+        layer._heads("k", far.view(2, 4, 64), 2, 4, 64, far.device)
+    near = torch.empty(1, dtype=torch.bfloat16, device="meta").as_strided((2, 256), ((1 << 31) - 8, 1))
+    assert layer._rows("x", near, 2, 256, near.device) == (1 << 31) - 8
+    assert layer._rows("x", far[:1], 1, 256, far.device) == 256
