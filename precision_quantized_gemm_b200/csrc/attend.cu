@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
   if (blockIdx.x >= share.ctas || share.total == 0) return;
   const int share_begin = share.begin(blockIdx.x), share_end = share.begin(blockIdx.x + 1);
   uint32_t phase = 0;  // bit i: parity of the ring stage's next wait
-  bool ok = true, drained = false;
+  bool ok = true;
 
   Piece x = find_piece(p, sched, ROWS, share_begin, share_end);
 #pragma unroll 1
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
     }
 
 #pragma unroll 1
-    for (int blk = warp; blk < nblk; blk += WARPS) {
+    for (int blk = ok ? warp : nblk; blk < nblk; blk += WARPS) {
       const int st = (blk / WARPS) % kStages;
       const uint32_t kb = ring + st * S::kStage, vb = kb + S::kCodes, sb = scale_ring + st * S::kScale;
       const int pos0 = begin + blk * kBlock;
@@ -291,10 +291,18 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
           for (int e = 0; e < 2; ++e)
             seen[i][e] = (uint32_t)(seen_bits(p, tok[i][e], end - pos0, past - pos0, drafted[i][e]) >> g);
       }
-      if (ok) ok = mbar_wait(bar + st, (phase >> st) & 1, p.err, p.wait_ns);
+      ok = __all_sync(0xffffffffu, mbar_wait(bar + st, (phase >> st) & 1, p.err, p.wait_ns));
+      if (!ok) {
+        // a wait ran out: the copies still in flight, this block's and the
+        // next ones', land before shared memory is given up (bounded as well);
+        // a stage's phase is the one that has not been passed
+        for (int i = 0; i < kStages; ++i) {
+          const int s = (blk / WARPS + i) % kStages;
+          if (blk + i * WARPS < nblk) (void)mbar_wait(bar + s, (phase >> s) & 1, p.err, p.wait_ns);
+        }
+        break;
+      }
       phase ^= 1u << st;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       {
         float a, b;
         value_scale(lds4(sb + kBlock * 4 + lane * 4), a, b);
@@ -437,13 +445,6 @@ __global__ void __launch_bounds__(kRowsWarps<NR> * 32, 1)
         next_page = page_of(ahead);
       }
     }
-    if (!ok && !drained) {
-      drained = true;
-      // a wait ran out: the copies still in flight land before shared memory
-      // is given up (bounded as well)
-      for (int i = 0; i < kStages; ++i) (void)mbar_wait(bar + i, (phase >> i) & 1, p.err, p.wait_ns);
-    }
-
     // the warps' results meet, each in its own ring with its own reference
 #pragma unroll
     for (int i = 0; i < NR; ++i)
