@@ -509,8 +509,11 @@ qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, 
  * NaN row that it sees, key or value, makes its out and lse NaN.
  * Device values are taken within bounds: offsets to [0, tokens], kv_len to
  * [0, max_pages * page_size], pages to [0, pages); drafted tokens past max_q
- * get no output.  batch <= 1024, max_q <= QGEMM_ATTEND_MAX_Q
- * (QG_ERR_UNSUPPORTED).
+ * get no output.  batch <= 1024, max_q <= QGEMM_ATTEND_MAX_Q, and what the
+ * sizes allow in positions of a sequence (max_pages * page_size) and in units
+ * of work (128 positions of 128 rows of one key head, a row being one query
+ * head of one token; with at most 24 rows, 32 for heads of 64, 64 positions
+ * of 8 or more) below 2^31 (QG_ERR_UNSUPPORTED).
  * A value scale below 2^-80 (values below 4e-22, or a place that was never
  * written) counts as 2^-80; where those that a token sees lie more than 2^100
  * apart, the share of the smaller ones may be lost.

@@ -41,14 +41,26 @@ long long rows_per_key_head(const qg_cache* c, const qg_attend* a) {
   return (long long)a->max_q * (a->q_heads / c->kv_heads);
 }
 
-// Rows per key head of the call's mean sequence: what its kernel goes by.
+// Units of work that the sizes of a call allow, cut for so many rows per key
+// head; counted in 32 bits by the kernels.
+bool units_fit(const qg_cache* c, const qg_attend* a, int rows) {
+  const qg::AttendSplit split = qg::attend_split(rows, c->head_dim);
+  const long long most = (long long)std::min(a->max_q, a->tokens) * (a->q_heads / c->kv_heads);
+  const double tiles = (double)((most + split.tile_rows - 1) / split.tile_rows);
+  const double units = (double)a->max_pages * c->page_size / split.unit + 1;
+  return units * tiles * c->kv_heads * a->batch <= 0x7fffff00;
+}
+
+// Rows per key head that a call's kernel goes by: those of its mean sequence.
 // Either kernel takes sequences of any number of tokens, and max_q may be far
 // above most of them.  8192 positions, 64 query and 8 key heads of 128, by
 // the mean and by max_q: 64 single tokens (max_q 64) 182 and 344 us, 63 and
-// one of 32 240 and 404 us, 63 and one of 129 408 and 459 us.
-int mean_rows(const qg_cache* c, const qg_attend* a) {
+// one of 32 240 and 404 us, 63 and one of 129 408 and 459 us.  Where the
+// smaller items would be too many to count, those of max_q.
+int kernel_rows(const qg_cache* c, const qg_attend* a) {
   const int mean = (int)(((long long)a->tokens + a->batch - 1) / a->batch);
-  return std::min(a->max_q, mean) * (a->q_heads / c->kv_heads);
+  const int rows = std::min(a->max_q, mean) * (a->q_heads / c->kv_heads);
+  return units_fit(c, a, rows) ? rows : (int)rows_per_key_head(c, a);
 }
 
 qg_status check_attend(const qg_cache* c, const qg_attend* a) {
@@ -67,11 +79,9 @@ qg_status check_attend(const qg_cache* c, const qg_attend* a) {
   if (a->tree_mask && (!aligned(a->tree_mask, 8) || a->mask_words <= 0)) return QG_ERR_INVALID_ARG;
   if (!(a->scale > -3.0e38f && a->scale < 3.0e38f)) return QG_ERR_INVALID_ARG;
   if (a->batch > qg::kAttendMaxBatch || a->max_q > QGEMM_ATTEND_MAX_Q) return QG_ERR_UNSUPPORTED;
-  // positions of a sequence and units of work (at least 64 positions of 8
-  // rows of one key head) are 32-bit
+  // positions of a sequence are 32-bit, like the units of work
   const double positions = (double)a->max_pages * c->page_size;
-  const double tiles = (double)rows_per_key_head(c, a) / 8 + 1;
-  if (rows_per_key_head(c, a) > 0x7fff0000 || positions > 0x7fffff00 || (positions / 64 + 1) * tiles * c->kv_heads * a->batch > 0x7fffff00)
+  if (rows_per_key_head(c, a) > 0x7fff0000 || positions > 0x7fffff00 || !units_fit(c, a, kernel_rows(c, a)))
     return QG_ERR_UNSUPPORTED;
   return QG_OK;
 }
@@ -286,7 +296,7 @@ qg_status qgemm_attend(const qg_cache* c, const qg_attend* a, void* workspace, s
   p.err = st.err;
   p.wait_ns = st.wait_ns;
   CUtensorMap tk, tv;
-  const int rows = mean_rows(c, a);
+  const int rows = kernel_rows(c, a);
   if (!qg::attend_tiles(rows, c->head_dim)) {
     const uint64_t all = (uint64_t)c->pages * c->kv_heads * c->page_size;
     if (!qg::make_row_tmap(&tk, c->k, c->head_dim, all, p.box_rows)) return QG_ERR_CUDA;

@@ -664,6 +664,11 @@ int tile_rows_of(int wanted, int head_dim) {
 
 }  // namespace
 
+AttendSplit attend_split(int rows, int head_dim) {
+  const int tile_rows = tile_rows_of(rows, head_dim);
+  return {tile_rows, tile_rows == kTileRows ? kTilePos : kUnit};
+}
+
 bool attend_tiles(int rows, int head_dim) { return tile_rows_of(rows, head_dim) == kTileRows; }
 
 size_t attend_workspace(int head_dim, int rows_max, int sms) {

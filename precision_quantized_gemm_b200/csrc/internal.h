@@ -114,6 +114,11 @@ struct AttendParams {
 };
 constexpr int kAttendMaxBatch = 1024;
 size_t attend_workspace(int head_dim, int rows_max, int sms);
+// How a call's work is cut: rows of an item, positions of a unit.
+struct AttendSplit {
+  int tile_rows, unit;
+};
+AttendSplit attend_split(int rows, int head_dim);
 bool attend_tiles(int rows, int head_dim);  // whether the tile kernel takes so many rows per key head
 cudaError_t launch_attend(AttendParams p, void* workspace, const uint8_t* k, const uint8_t* v, const CUtensorMap* tk,
                           const CUtensorMap* tv, int rows, int head_dim, bool int8, int sms, cudaStream_t st, bool pdl);

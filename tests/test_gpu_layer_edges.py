@@ -255,3 +255,15 @@ def test_buffers_of_another_device_are_refused():
     b = Batch(qg.QG_FP8_DYNAMIC, [20], [1], 2, 2, 64, 16, seed=1, tree=False)
     with pytest.raises(ValueError, match="workspace"):
         b.run(workspace=qg.Workspace("cpu"))
+
+
+def test_sizes_that_allow_more_units_than_the_small_items_may_have():
+    """1024 single tokens under a max_q of 256 and a table of 131072 positions: tiles, where a max_q of 1 takes the
+    other kernel."""
+    r = np.random.default_rng(0)
+    b = Batch(qg.QG_FP8_DYNAMIC, [int(a) for a in r.integers(1, 60, 1024)], [1] * 1024, 64, 8, 128, 64, seed=1, tree=False)
+    wide = torch.full((1024, 2048), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    b.check(*b.run(max_q=256), rows=1)
+    b.check(*b.run(max_q=1), rows=1)

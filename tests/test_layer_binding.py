@@ -68,3 +68,21 @@ def test_strides_past_32_bits_are_refused():
     near = torch.empty(1, dtype=torch.bfloat16, device="meta").as_strided((2, 256), ((1 << 31) - 8, 1))
     assert layer._rows("x", near, 2, 256, near.device) == (1 << 31) - 8
     assert layer._rows("x", far[:1], 1, 256, far.device) == 256
+
+
+def _sizes(batch, tokens, max_q, positions, q_heads=64, kv_heads=8, dim=128):
+    p = 0x100000  # stands in for every address
+    c = qg.qg_cache(format=0, pages=64, page_size=64, kv_heads=kv_heads, head_dim=dim, k=p, v=p, k_scale=p, v_scale=p)
+    a = qg.qg_attend(q=p, out=p, q_offsets=p, kv_len=p, page_table=p, ldq=q_heads * dim, ldo=q_heads * dim,
+                     q_heads=q_heads, batch=batch, tokens=tokens, max_q=max_q, max_pages=positions // 64, scale=0.125)
+    return qg.qgemm_attend(c, a, p, 1 << 30, None)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would launch on stand-in pointers")
+def test_what_fits_is_not_refused():
+    """Units of work are counted as the kernel cuts them: 16 row tiles of 128, not 256 of 8, and no more tokens than
+    there are."""
+    assert _sizes(1024, 1024 * 256, 256, 131072) != qg.QG_ERR_UNSUPPORTED   # 134 million units
+    assert _sizes(1024, 1024, 256, 131072) != qg.QG_ERR_UNSUPPORTED
+    assert _sizes(1024, 1024 * 256, 256, 1 << 25) == qg.QG_ERR_UNSUPPORTED  # 34 billion
+    assert _sizes(1024, 1024, 256, 1 << 25) == qg.QG_ERR_UNSUPPORTED
