@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) qg_attend_tile_kernel(const u
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   y[e] = fmaf(__uint_as_float(q[4 * k + e]), of[e >> 1], __uint_as_float(o[4 * k + e]) * f[e >> 1]);
-                if (!*static_cast<const volatile int*>(&x.whole)) {
+                if (!whole) {
                   // as the fragments lie: whole lines (the merge knows)
                   reinterpret_cast<float4*>(part)[((rw >> 4) * (D / 8) + c / 8 + k) * 32 + lane] =
                       make_float4(y[0], y[1], y[2], y[3]);
