@@ -267,3 +267,16 @@ def test_sizes_that_allow_more_units_than_the_small_items_may_have():
     b.table = wide
     b.check(*b.run(max_q=256), rows=1)
     b.check(*b.run(max_q=1), rows=1)
+
+
+def test_tokens_past_the_end():
+    """A sequence whose end offset lies past the tokens has those that are there: its last positions, in order."""
+    b = Batch(qg.QG_FP8_DYNAMIC, [200, 77], [2, 3], 8, 2, 128, 16, seed=5, tree=False)
+    b.offs += 4  # 4, 6, 9 of 8 rows
+    out, lse = torch.full_like(b.q, 7.0), torch.full((8, 8), 7.0, device="cuda")
+    qg.attend(b.cache, b.q, b.offs, b.lens_t, b.table, out=out, lse=lse, max_q=3)
+    assert (out[:4] == 7).all() and (lse[:4] == 7).all()
+    # the check wants its rows from 0 on and three behind the last
+    pad = lambda t: torch.cat([t[4:], torch.full_like(t[:3], 7.0)])  # noqa: E731
+    b.q, b.ns, b.T = pad(b.q), [2, 2], 4
+    b.check(pad(out), pad(lse))
