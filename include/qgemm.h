@@ -506,7 +506,9 @@ qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, 
  * A token that sees nothing gets zeros and lse -inf.  Rows of out and lse that
  * belong to no sequence are left as they were; out and lse overlap none of the
  * inputs.  What a token does not see does not reach it, NaN rows included; a
- * NaN row that it sees, key or value, makes its out and lse NaN.
+ * NaN row that it sees, key or value, makes its out and lse NaN.  (Codes are
+ * finite, as qgemm_cache_write makes them: in a cache filled by other means an
+ * e4m3 NaN code among a sequence's positions reaches every token.)
  * Device values are taken within bounds: offsets to [0, tokens], kv_len to
  * [0, max_pages * page_size], pages to [0, pages); drafted tokens past max_q
  * get no output.  batch <= 1024, max_q <= QGEMM_ATTEND_MAX_Q, and what the
@@ -518,7 +520,8 @@ qg_status qgemm_cache_read(const qg_cache* c, const int32_t* slots, int tokens, 
  * written) counts as 2^-80; where those that a token sees lie more than 2^100
  * apart, the share of the smaller ones may be lost.
  * The queries are exact down to 2^-28 of their row's largest; weights are
- * f16 relative to the largest |weight x value scale|, everything else fp32. */
+ * f16 relative to the largest |weight x value scale| (off by 2^-31 of it at
+ * most where that is more than 2^-12 of their own), everything else fp32. */
 typedef struct {
   const void* q;            /* bf16 [tokens, ldq], head h at h * head_dim            */
   void* out;                /* bf16 [tokens, ldo]                                    */
