@@ -59,8 +59,9 @@ def test_log_sum_of_zero_scales(Hq, D):
 @pytest.mark.parametrize("Hq", [4, 64])
 def test_many_weights_far_below_the_largest(fmt, D, Hq):
     """One position 25.5 powers of two above 16384 others that it shares a reference with: the others are all that
-    reaches the channels in which its value is 0.  A weight is off by 2^-32 of the largest (f16 near its lowest),
-    the sum of the others by as much for each."""
+    reaches the channels in which its value is 0.  A weight is off by 2^-31 of the largest: half of f16's lowest
+    step, 2^-25, over a largest weight of 2^6 to 2^7 (tiles: their reference may lie up to 1 above the largest
+    score).  The sum of the others is off by as much for each."""
     n, page, B, H = 16384, 1024, 300, 2
     cache = qg.Cache(fmt, n // page, page, H, D)
     g = _gen(D + Hq)
@@ -82,7 +83,7 @@ def test_many_weights_far_below_the_largest(fmt, D, Hq):
     assert 2.0 ** -12 < o[1] < 2.0 ** -11
     # exponents of 26 hold 2^-19: the scores' roundings, and the rest as for ordinary inputs
     rel = F16 + 2.0 ** -17 + n * F32
-    _close(out, np.broadcast_to(o, out.shape), BF16 * np.abs(o) + rel * mag + n * 2.0 ** -32, "out")
+    _close(out, np.broadcast_to(o, out.shape), BF16 * np.abs(o) + rel * mag + n * 2.0 ** -31, "out")
     # the sum is kept in 16 chains or more a row (tiles: 2 groups x 4 lanes x 2 elements), each of at most n / 16
     # additions that round by half a unit of the sum so far, which is at most the whole: n / 16 F32 of it.  (Beside
     # the largest, a term of 2^-25.5 of it is under half a unit and lost: 1 / 16 of 16384 x 2^-25.5 is 2.2e-5.)
